@@ -224,14 +224,19 @@ def _plain_round_mx(x):
     largest magnitude less 2 (the exponent of e2m1's largest, 6), and larger values than 6 become 6."""
     b = x.reshape(x.shape[0], -1, 32)
     e = torch.frexp(b.abs().amax(2, keepdim=True))[1] - 3
-    v = torch.ldexp(b, -e)
+    v = b * _power(-e)
     m = v.abs()
     code = ((m > 0.25).int() + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0))
-    return (torch.ldexp(_e2m1(x.device)[code], e) * torch.where(v < 0, -1.0, 1.0)).reshape(x.shape)
+    return (_e2m1(x.device)[code] * _power(e) * torch.where(v < 0, -1.0, 1.0)).reshape(x.shape)
 
 
 def _e2m1(device):
     return torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=device)
+
+
+def _power(e):
+    """FP32 2^e, exactly, for -126 <= e <= 127."""
+    return ((e + 127) << 23).view(torch.float32)
 
 
 def _plain_mxq(s):
@@ -242,7 +247,7 @@ def _plain_mx_values(q, scales):
     """FP32 values of packed codes, low nibble first, and their biased exponents."""
     code = torch.stack([q & 15, q >> 4], -1).flatten(-2).int()
     v = _e2m1(q.device)[code & 7] * torch.where(code > 7, -1.0, 1.0)
-    v = v.reshape(*q.shape[:-1], -1, 32) * torch.exp2(scales[..., : q.shape[-1] // 16].float() - 127.0)[..., None]
+    v = v.reshape(*q.shape[:-1], -1, 32) * _power(scales[..., : q.shape[-1] // 16].int() - 127)[..., None]
     return v.flatten(-2)
 
 
