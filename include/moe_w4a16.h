@@ -401,6 +401,120 @@ moe_status_t moe_w4a16_down(const moe_weights_t* h, const uint16_t* a, int32_t T
 moe_status_t moe_swiglu(const uint16_t* h, int64_t rows, int32_t inter, uint16_t* a,
                         moe_stream_t stream);
 
+/* ---- operators around the layer --------------------------------------------
+ *
+ * The router that makes topk_ids and topk_w, the experts' products for
+ * weights that are not INT4 (BF16 or FP16 checkpoints, training) and for
+ * MXFP4 weights. They need no handle and no workspace, run on the current
+ * device (stream must be one of its streams) and each enqueue one kernel.
+ * Outputs must not overlap inputs.
+ *
+ * Groups of rows: expert e holds rows [offsets[e], offsets[e + 1]) of a
+ * matrix of M rows; offsets is device int32 [E + 1] and must not decrease.
+ * An expert may hold no row, and rows before offsets[0] or behind offsets[E]
+ * belong to none: they are not read, and their output rows are left as they
+ * were. Bounds are clamped to [0, M]; with offsets that decrease no memory
+ * outside the arguments is touched, but the outputs are unspecified. The
+ * offsets of a routing buffer (off_offsets) are such offsets for the rows
+ * moe_permute writes.
+ *
+ * Leading dimensions (ld) and strides count values of the matrix; ld is a
+ * multiple of 8 and at most 2^21, pointers to matrices are 16-byte aligned.
+ * Products accumulate in FP32 and round once to out_dtype. */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 };
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* The topk experts of each token and their weights, from router logits.
+ * Score s = softmax(logits) or sigmoid(logits). The experts of largest logit
+ * are chosen, or with a bias those of largest s + bias (computed in FP64);
+ * largest first, the lowest index of equal ones. Weight: scale * s, or with
+ * renorm scale * s / (sum of the chosen s); the bias takes no part in it.
+ * A logit of -inf or NaN, and a bias of -inf or NaN, take their expert out;
+ * +inf counts as the largest FP32 value. A token with fewer than topk experts
+ * left gets id -1 (which routes nowhere) and weight 0 in the places behind.
+ *   logits    device [T, E] of dtype, rows ld values apart (any alignment of
+ *             the type)
+ *   bias      device float [E] or NULL
+ *   topk_ids  device int32 [T, topk], topk_w device float [T, topk]
+ * E 1..4096, topk 1..min(E, 64). Errors: INVALID_ARG, HIP. */
+moe_status_t moe_router_topk(const void* logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
+                             int32_t topk, int32_t score, const float* bias, int32_t renorm,
+                             float scale, int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/* Gradient of the logits for the ids moe_router_topk chose (distinct in a
+ * row; -1 and other ids outside [0, E) take no part) and the gradient
+ * d_topk_w (device float [T, topk]) of their weights; the choice itself and
+ * the bias have no gradient.
+ *   d_logits  device [T, E] of dtype, rows d_ld values apart, fully written
+ * Errors: as moe_router_topk. */
+moe_status_t moe_router_topk_grad(const void* logits, int32_t dtype, int64_t ld, int32_t T,
+                                  int32_t E, int32_t topk, int32_t score, int32_t renorm,
+                                  float scale, const int32_t* topk_ids, const float* d_topk_w,
+                                  void* d_logits, int64_t d_ld, moe_stream_t stream);
+
+/* Grouped product: out[r] = a[r] . w[e]^T for every row r of expert e.
+ *   a    device [M, K], w device [E, N, K] of dtype (BF16 or FP16); experts
+ *        w_stride values apart (0: one matrix for all)
+ *   out  device [M, N] of out_dtype (BF16, FP16 or FP32)
+ * N and K are multiples of 8 up to 2^20, M at most 2^30, E 1..4096.
+ * Errors: INVALID_ARG, HIP. */
+moe_status_t moe_grouped_gemm(const void* a, int64_t a_ld, const void* w, int64_t w_stride,
+                              int64_t w_ld, int32_t dtype, const int32_t* offsets, int32_t E,
+                              int32_t M, int32_t N, int32_t K, void* out, int64_t out_ld,
+                              int32_t out_dtype, moe_stream_t stream);
+
+/* Gradient of the grouped product's input: da[r] = dy[r] . w[e].
+ *   dy   device [M, N], w device [E, N, K] of dtype, da device [M, K] of
+ *        out_dtype. Otherwise as moe_grouped_gemm. */
+moe_status_t moe_grouped_gemm_dgrad(const void* dy, int64_t dy_ld, const void* w,
+                                    int64_t w_stride, int64_t w_ld, int32_t dtype,
+                                    const int32_t* offsets, int32_t E, int32_t M, int32_t N,
+                                    int32_t K, void* da, int64_t da_ld, int32_t out_dtype,
+                                    moe_stream_t stream);
+
+/* Gradient of the grouped product's weights: dw[e] = sum over the rows r of
+ * e of dy[r]^T a[r]; 0 for an expert without rows.
+ *   dy   device [M, N], a device [M, K] of dtype
+ *   dw   device [E, N, K] of out_dtype, fully written, experts dw_stride >=
+ *        (N - 1) * dw_ld + K values apart. Otherwise as moe_grouped_gemm. */
+moe_status_t moe_grouped_gemm_wgrad(const void* dy, int64_t dy_ld, const void* a, int64_t a_ld,
+                                    int32_t dtype, const int32_t* offsets, int32_t E, int32_t M,
+                                    int32_t N, int32_t K, void* dw, int64_t dw_stride,
+                                    int64_t dw_ld, int32_t out_dtype, moe_stream_t stream);
+
+/* MXFP4 rows of K values (K a multiple of 32): codes uint8 [rows, K/2], two
+ * FP4 (e2m1) codes a byte, the lower nibble first along K, and scales uint8
+ * [rows, moe_mx_scale_cols(K)], one E8M0 byte (2^(byte - 127), 255 = NaN) per
+ * 32 values, a row padded to a multiple of 16 bytes (the padding is written
+ * as 0 and read as nothing). Both are dense. 0 for a bad K. */
+int32_t moe_mx_scale_cols(int32_t K);
+
+/* Quantise rows to MXFP4. A block's scale is 2^(floor(log2 m) - 2) for its
+ * largest magnitude m (at least 2^-127); values over it are rounded to the
+ * nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (the even code of two as near), and
+ * above 6 to 6. A block that holds a NaN or an infinity becomes NaN (scale
+ * byte 255, codes 0).
+ *   x  device [rows, K] of dtype (BF16, FP16 or FP32), rows ld values apart,
+ *      ld a multiple of 8
+ * Errors: INVALID_ARG, HIP. */
+moe_status_t moe_mx_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32_t K,
+                          uint8_t* q, uint8_t* scales, moe_stream_t stream);
+
+/* The values of MXFP4 rows, each rounded once to dtype. */
+moe_status_t moe_mx_dequant(const uint8_t* q, const uint8_t* scales, int64_t rows, int32_t K,
+                            void* out, int32_t dtype, int64_t ld, moe_stream_t stream);
+
+/* Grouped product of MXFP4 rows and MXFP4 weights: out[r] = a[r] . w[e]^T on
+ * their values, multiplied in FP4 by the matrix cores (scaled MFMA).
+ *   aq uint8 [M, K/2], a_scales uint8 [M, moe_mx_scale_cols(K)]
+ *   wq uint8 [E, N, K/2], w_scales uint8 [E, N, moe_mx_scale_cols(K)]
+ *   out  device [M, N] of out_dtype, rows out_ld values apart
+ * K is a multiple of 32, N of 8. Otherwise as moe_grouped_gemm. */
+moe_status_t moe_mx_grouped_gemm(const uint8_t* aq, const uint8_t* a_scales, const uint8_t* wq,
+                                 const uint8_t* w_scales, const int32_t* offsets, int32_t E,
+                                 int32_t M, int32_t N, int32_t K, void* out, int64_t out_ld,
+                                 int32_t out_dtype, moe_stream_t stream);
+
 /* ---- inspection ------------------------------------------------------------ */
 
 /* Dequantise one expert's prepared matrix back to canonical order with the

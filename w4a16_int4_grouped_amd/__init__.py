@@ -36,6 +36,9 @@ MODES = {"indexed": MOE_MODE_INDEXED, "contiguous": MOE_MODE_CONTIGUOUS, "masked
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
 MOE_SCALE_BF16 = 1
+MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 MOE_PACK_INT32_LOW_NIBBLE_FIRST_K = 1
 
 EXPORTS = [
@@ -44,6 +47,8 @@ EXPORTS = [
     "moe_routing_layout", "moe_align", "moe_align_ep", "moe_permute", "moe_workspace_bytes", "moe_w4a16_indexed",
     "moe_w4a16_indexed_noalloc", "moe_w4a16_contiguous", "moe_w4a16_masked", "moe_w4a16_gate_up", "moe_w4a16_down", "moe_swiglu",
     "moe_dequant_weights", "moe_describe",
+    "moe_router_topk", "moe_router_topk_grad", "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
+    "moe_mx_scale_cols", "moe_mx_quant", "moe_mx_dequant", "moe_mx_grouped_gemm",
     "moe_profile_enable", "moe_profile_reset", "moe_profile_read",
 ]
 
@@ -96,6 +101,7 @@ def lib() -> ctypes.CDLL:
                            " (there is no CPU fallback)")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    F32 = ctypes.c_float
     sig = {
         "moe_abi_version": (S, []),
         "moe_last_error": (ctypes.c_char_p, []),
@@ -120,6 +126,15 @@ def lib() -> ctypes.CDLL:
         "moe_swiglu": (S, [P, I64, I32, P, P]),
         "moe_dequant_weights": (S, [P, I32, I32, P, P]),
         "moe_describe": (S, [P, I32, I32, I32, I32, ctypes.POINTER(Tuning), ctypes.c_char_p, SZ]),
+        "moe_router_topk": (S, [P, I32, I64, I32, I32, I32, I32, P, I32, F32, P, P, P]),
+        "moe_router_topk_grad": (S, [P, I32, I64, I32, I32, I32, I32, I32, F32, P, P, P, I64, P]),
+        "moe_grouped_gemm": (S, [P, I64, P, I64, I64, I32, P, I32, I32, I32, I32, P, I64, I32, P]),
+        "moe_grouped_gemm_dgrad": (S, [P, I64, P, I64, I64, I32, P, I32, I32, I32, I32, P, I64, I32, P]),
+        "moe_grouped_gemm_wgrad": (S, [P, I64, P, I64, I32, P, I32, I32, I32, I32, P, I64, I64, I32, P]),
+        "moe_mx_scale_cols": (I32, [I32]),
+        "moe_mx_quant": (S, [P, I32, I64, I64, I32, P, P, P]),
+        "moe_mx_dequant": (S, [P, P, I64, I32, P, I32, I64, P]),
+        "moe_mx_grouped_gemm": (S, [P, P, P, P, P, I32, I32, I32, I32, P, I64, I32, P]),
         "moe_profile_enable": (S, [S]),
         "moe_profile_reset": (None, []),
         "moe_profile_read": (S, [ctypes.c_char_p, SZ]),
@@ -349,6 +364,261 @@ def swiglu(h, out=None, stream=None):
     if out is None:
         out = torch.empty((rows, two_i // 2), dtype=torch.bfloat16, device=h.device)
     check(lib().moe_swiglu(_ptr(h), rows, two_i // 2, _ptr(out), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around the layer
+# ---------------------------------------------------------------------------
+
+_DTYPES = None
+
+
+def _dtype(t) -> int:
+    """MOE_DTYPE_* of a torch dtype."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
+    code = _DTYPES.get(t)
+    if code is None:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{t}: bfloat16, float16 or float32")
+    return code
+
+
+def _need(ok, msg):
+    if not ok:
+        raise MoeError(MOE_ERR_INVALID_ARG, msg)
+
+
+def _matrix(t, name, dtype=None, device=None, shape=None):
+    """Checks a tensor's rows: on the GPU (the first operand's), of a dtype
+    and shape, values of a row adjacent. Returns the row distance."""
+    _need(t.is_cuda, f"{name}: not on a GPU")
+    _need(device is None or t.device == device, f"{name}: on {t.device}, the first operand on {device}")
+    _need(dtype is None or t.dtype == dtype, f"{name}: {t.dtype}, expected {dtype}")
+    _need(shape is None or tuple(t.shape) == shape, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    # a dimension of one element has no meaningful stride
+    _need(t.stride(-1) == 1 or t.shape[-1] <= 1, f"{name}: the values of a row are not adjacent")
+    rows, width = t.shape[-2], t.shape[-1]
+    return t.stride(-2) if rows > 1 else max(width, (width + 7) // 8 * 8)
+
+
+def _dense(t, name, dtype, device, shape):
+    import torch
+    _need(t.is_cuda and t.device == device, f"{name}: not on the first operand's GPU")
+    _need(t.dtype == dtype, f"{name}: {t.dtype}, expected {dtype}")
+    _need(tuple(t.shape) == shape, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    _need(t.is_contiguous(), f"{name}: not contiguous")
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) on `device`: on `stream`, or on its current stream."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, _stream(stream)))
+
+
+def router_topk(logits, topk, score="softmax", bias=None, renorm=False, scale=1.0, out=None, stream=None):
+    """(ids int32, weights float32), both [T, topk]: each token's experts of
+    largest logit (with `bias`, float32 [E]: of largest score + bias, in FP64),
+    largest first, equal ones by index. Weight: scale * score, with `renorm`
+    over the sum of the chosen scores. A logit of -inf or NaN takes its expert
+    out for the token; places without an expert hold id -1 and weight 0, which
+    the layer routes nowhere. logits [T, E] bf16, fp16 or fp32; `out` may give
+    the two tensors."""
+    import torch
+    _need(logits.dim() == 2, "logits: [T, E]")
+    T, E = logits.shape
+    ld = _matrix(logits, "logits")
+    dev = logits.device
+    _need(score in SCORES, f"score {score!r}: softmax or sigmoid")
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, dev, (E,))
+    if out is None:
+        ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        w = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    else:
+        ids, w = out
+        _dense(ids, "ids", torch.int32, dev, (T, topk))
+        _dense(w, "weights", torch.float32, dev, (T, topk))
+    _call(lib().moe_router_topk, dev, stream, _ptr(logits), _dtype(logits.dtype), max(ld, E), T, E, topk,
+          SCORES[score], _ptr(bias), int(bool(renorm)), float(scale), _ptr(ids), _ptr(w))
+    return ids, w
+
+
+def router_topk_grad(logits, ids, d_w, score="softmax", renorm=False, scale=1.0, out=None, stream=None):
+    """Gradient [T, E] of the logits (their dtype) for the ids that
+    router_topk chose with the same score, renorm and scale, and the gradient
+    d_w (float32 [T, topk]) of their weights."""
+    import torch
+    _need(logits.dim() == 2 and ids.dim() == 2, "logits: [T, E], ids: [T, topk]")
+    T, E = logits.shape
+    ld = _matrix(logits, "logits")
+    dev = logits.device
+    topk = ids.shape[1]
+    _need(score in SCORES, f"score {score!r}: softmax or sigmoid")
+    _dense(ids, "ids", torch.int32, dev, (T, topk))
+    _dense(d_w, "d_w", torch.float32, dev, (T, topk))
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    o_ld = _matrix(out, "out", logits.dtype, dev, (T, E))
+    _call(lib().moe_router_topk_grad, dev, stream, _ptr(logits), _dtype(logits.dtype), max(ld, E), T, E, topk,
+          SCORES[score], int(bool(renorm)), float(scale), _ptr(ids), _ptr(d_w), _ptr(out), max(o_ld, E))
+    return out
+
+
+def _groups(offsets, device, E=None):
+    import torch
+    _need(offsets.dim() == 1 and offsets.numel() >= 2, "offsets: [E + 1]")
+    E = offsets.numel() - 1 if E is None else E
+    _dense(offsets, "offsets", torch.int32, device, (E + 1,))
+    return E
+
+
+def _weights(w, dtype, device):
+    _need(w.dim() == 3, "w: [E, N, K]")
+    ld = _matrix(w, "w", dtype, device)
+    return ld, (w.stride(0) if w.shape[0] > 1 else 0)
+
+
+def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
+    """out[r] = a[r] . w[e]^T for the rows r in [offsets[e], offsets[e + 1]).
+
+    a [M, K] and w [E, N, K] bf16 or fp16, offsets int32 [E + 1] on the GPU,
+    not decreasing; out [M, N] of out_dtype (default a's; fp32 as well). Rows
+    may be apart (strides of a multiple of 8). Rows of no expert are left as
+    they are in `out`. N and K are multiples of 8."""
+    import torch
+    _need(a.dim() == 2 and w.dim() == 3, "a: [M, K], w: [E, N, K]")
+    M, K = a.shape
+    E, N, Kw = w.shape
+    _need(K == Kw, f"a has {K} columns, w {Kw}")
+    dev = a.device
+    a_ld = _matrix(a, "a")
+    w_ld, w_stride = _weights(w, a.dtype, dev)
+    _groups(offsets, dev, E)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or a.dtype, device=dev)
+    o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
+    _call(lib().moe_grouped_gemm, dev, stream, _ptr(a), a_ld, _ptr(w), w_stride, w_ld, _dtype(a.dtype), _ptr(offsets),
+          E, M, N, K, _ptr(out), o_ld, _dtype(out.dtype))
+    return out
+
+
+def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
+    """Gradient of grouped_gemm's `a`: out[r] = dy[r] . w[e], [M, K]."""
+    import torch
+    _need(dy.dim() == 2 and w.dim() == 3, "dy: [M, N], w: [E, N, K]")
+    M, N = dy.shape
+    E, Nw, K = w.shape
+    _need(N == Nw, f"dy has {N} columns, w {Nw} rows")
+    dev = dy.device
+    y_ld = _matrix(dy, "dy")
+    w_ld, w_stride = _weights(w, dy.dtype, dev)
+    _groups(offsets, dev, E)
+    if out is None:
+        out = torch.empty((M, K), dtype=out_dtype or dy.dtype, device=dev)
+    o_ld = _matrix(out, "out", out_dtype, dev, (M, K))
+    _call(lib().moe_grouped_gemm_dgrad, dev, stream, _ptr(dy), y_ld, _ptr(w), w_stride, w_ld, _dtype(dy.dtype),
+          _ptr(offsets), E, M, N, K, _ptr(out), o_ld, _dtype(out.dtype))
+    return out
+
+
+def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
+    """Gradient of grouped_gemm's `w`: out[e] = dy[rows of e]^T . a[rows of e],
+    [E, N, K]; 0 for an expert without rows."""
+    import torch
+    _need(dy.dim() == 2 and a.dim() == 2 and dy.shape[0] == a.shape[0], "dy: [M, N], a: [M, K]")
+    M, N = dy.shape
+    K = a.shape[1]
+    dev = dy.device
+    y_ld = _matrix(dy, "dy")
+    a_ld = _matrix(a, "a", dy.dtype, dev)
+    E = _groups(offsets, dev)
+    if out is None:
+        out = torch.empty((E, N, K), dtype=out_dtype or dy.dtype, device=dev)
+    o_ld = _matrix(out, "out", out_dtype, dev, (E, N, K))
+    stride = out.stride(0) if E > 1 else ((N - 1) * o_ld + K + 7) // 8 * 8
+    _call(lib().moe_grouped_gemm_wgrad, dev, stream, _ptr(dy), y_ld, _ptr(a), a_ld, _dtype(dy.dtype), _ptr(offsets),
+          E, M, N, K, _ptr(out), stride, o_ld, _dtype(out.dtype))
+    return out
+
+
+def mx_scale_cols(K) -> int:
+    """Bytes of a row of MXFP4 scales: K / 32 rounded up to a multiple of 16."""
+    n = lib().moe_mx_scale_cols(K)
+    if n == 0:
+        check(MOE_ERR_INVALID_ARG)
+    return n
+
+
+def mx_quant(x, out=None, stream=None):
+    """MXFP4 rows of x [..., K] (bf16, fp16 or fp32, K a multiple of 32):
+    (codes uint8 [..., K/2], the lower nibble first; scales uint8 [...,
+    mx_scale_cols(K)], one E8M0 byte per 32 values). More than two dimensions
+    must be dense; `out` may give the two tensors."""
+    import torch
+    _need(x.dim() >= 2, "x: [..., K]")
+    K = x.shape[-1]
+    ld = _matrix(x, "x")
+    _need(x.dim() == 2 or x.is_contiguous(), "x: more than two dimensions must be contiguous")
+    rows = x.numel() // K if K else 0
+    cols = mx_scale_cols(K)
+    dev = x.device
+    lead = tuple(x.shape[:-1])
+    if out is None:
+        q = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=dev)
+        scales = torch.empty(lead + (cols,), dtype=torch.uint8, device=dev)
+    else:
+        q, scales = out
+        _dense(q, "codes", torch.uint8, dev, lead + (K // 2,))
+        _dense(scales, "scales", torch.uint8, dev, lead + (cols,))
+    _call(lib().moe_mx_quant, dev, stream, _ptr(x), _dtype(x.dtype), ld if x.dim() == 2 else K, rows, K, _ptr(q),
+          _ptr(scales))
+    return q, scales
+
+
+def mx_dequant(q, scales, dtype=None, out=None, stream=None):
+    """Values [..., K] of MXFP4 rows in `dtype` (default bf16)."""
+    import torch
+    _need(q.dim() >= 2, "codes: [..., K/2]")
+    K = 2 * q.shape[-1]
+    lead = tuple(q.shape[:-1])
+    dev = q.device
+    _dense(q, "codes", torch.uint8, dev, tuple(q.shape))
+    _dense(scales, "scales", torch.uint8, dev, lead + (mx_scale_cols(K),))
+    if out is None:
+        out = torch.empty(lead + (K,), dtype=dtype or torch.bfloat16, device=dev)
+    ld = _matrix(out, "out", dtype, dev, lead + (K,))
+    _need(out.dim() == 2 or out.is_contiguous(), "out: more than two dimensions must be contiguous")
+    _call(lib().moe_mx_dequant, dev, stream, _ptr(q), _ptr(scales), q.numel() * 2 // K, K, _ptr(out),
+          _dtype(out.dtype), ld if out.dim() == 2 else K)
+    return out
+
+
+def mx_grouped_gemm(aq, a_scales, wq, w_scales, offsets, out=None, out_dtype=None, stream=None):
+    """grouped_gemm on MXFP4 rows (aq uint8 [M, K/2]) and MXFP4 weights (wq
+    uint8 [E, N, K/2]) with their scales as mx_quant writes them; out [M, N]
+    of out_dtype (default bf16)."""
+    import torch
+    _need(aq.dim() == 2 and wq.dim() == 3, "aq: [M, K/2], wq: [E, N, K/2]")
+    M, E, N, K = aq.shape[0], wq.shape[0], wq.shape[1], 2 * aq.shape[1]
+    dev = aq.device
+    cols = mx_scale_cols(K)
+    _dense(aq, "aq", torch.uint8, dev, (M, K // 2))
+    _dense(a_scales, "a_scales", torch.uint8, dev, (M, cols))
+    _dense(wq, "wq", torch.uint8, dev, (E, N, K // 2))
+    _dense(w_scales, "w_scales", torch.uint8, dev, (E, N, cols))
+    _groups(offsets, dev, E)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
+    _call(lib().moe_mx_grouped_gemm, dev, stream, _ptr(aq), _ptr(a_scales), _ptr(wq), _ptr(w_scales), _ptr(offsets),
+          E, M, N, K, _ptr(out), o_ld, _dtype(out.dtype))
     return out
 
 
