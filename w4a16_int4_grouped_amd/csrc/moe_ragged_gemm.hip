@@ -3,6 +3,7 @@
 
 #include "moe_device.h"
 #include "moe_ragged.h"
+#include "moe_tile.h"
 
 namespace moe {
 namespace {
@@ -12,6 +13,7 @@ typedef __attribute__((address_space(3))) char lds_char_t;
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 enum Fmt : int { FMT_BF16 = 0, FMT_F16 = 1, FMT_MX = 2 };
@@ -19,23 +21,24 @@ enum Fmt : int { FMT_BF16 = 0, FMT_F16 = 1, FMT_MX = 2 };
 constexpr int kStageBytes = 128;          // contraction bytes of a row per step: 64 values, or 256 FP4 codes
 constexpr uint32_t kPastEnd = 0x80000000u; // an offset past every operand tile: the load gives 0
 
-template <int FMT>
-__device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
-  if constexpr (FMT == FMT_F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
-                                                  0, 0, 0);
-  else
-    return mfma16(a, b, c);
-}
-
-// D += A . B on one 16x16x128 tile of FP4 codes, byte KK of each lane's scale
-// word: lane l feeds 32 codes of row l%16 of A (column l%16 of B), its block
-// l/16 of the four.
-template <int KK>
-__device__ __forceinline__ f32x4_t mma_mx(u32x4_t a, u32x4_t b, f32x4_t c, int sa, int sb) {
-  const i32x8_t A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8_t B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, KK, sa, KK, sb);
+// D += A . B on one 32x32 tile (FP32 accumulate), 32 contraction bytes: 16
+// BF16 or FP16 values, or 64 FP4 codes. Lane l feeds row l%32 of A and column
+// l%32 of B with the 16 bytes of its half l/32; component 4k + i of D is row
+// 8k + 4 (l/32) + i, column l%32. FP4: times 2^(scale - 127) of byte SB of the
+// lane's scale words, one per 32 codes.
+template <int FMT, int SB>
+__device__ __forceinline__ f32x16_t mma(u32x4_t a, u32x4_t b, f32x16_t c, int sa, int sb) {
+  if constexpr (FMT == FMT_MX) {
+    const i32x8_t A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8_t B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, SB, sa, SB, sb);
+  } else if constexpr (FMT == FMT_F16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  }
 }
 
 // First row and row count of expert e, whatever the offsets hold: within [0, M].
@@ -47,9 +50,21 @@ __device__ __forceinline__ Group group_of(const RaggedParams& p, int e) {
   return Group{lo, min(max(p.offsets[e + 1], lo), p.M) - lo};
 }
 
+// Workgroup b's item of `total`: runs of G consecutive items (tiles that share
+// operands, and one XCD's L2) dealt round-robin to the XCDs, so that each gets
+// its part of large and small experts; -1 past the last. A run is an XCD's 32
+// CUs, less where that would leave XCDs without one. The grid needs total +
+// 8 * 32 workgroups.
+__device__ __forceinline__ int deal(int b, int total) {
+  const int G = min(max(total / 64, 1), 32);
+  const int idx = b >> 3, run = (idx / G) * 8 + (b & 7);
+  const int t = run * G + idx % G;
+  return t < total ? t : -1;
+}
+constexpr int kDealSlack = 8 * 32;
+
 // The tile of workgroup b among all experts' tiles of BJ rows x NI columns,
-// experts in order, a column's row tiles side by side, each XCD one
-// contiguous share. e < 0: none left. Every lane of a wave looks at one of 64
+// experts in order, a column's row tiles side by side. e < 0: none left. Every lane of a wave looks at one of 64
 // experts at a time.
 struct Tile {
   int e, it, jt;
@@ -61,7 +76,7 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, 
   for (int base = 0; base < p.E; base += 64) total += count(base + lane);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
-  const int t = xcd_remap_active(b, __builtin_amdgcn_readfirstlane(total) * NI);
+  const int t = deal(b, __builtin_amdgcn_readfirstlane(total) * NI);
   if (t < 0) return Tile{-1, 0, 0};
   int before = 0;
   for (int base = 0; base < p.E; base += 64) {
@@ -85,21 +100,45 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, 
   return Tile{-1, 0, 0};
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+// Buffer descriptor of `bytes` bytes from p: loads past the last read 0.
+__device__ __forceinline__ u32x4_t rsrc(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+
+// 16 bytes per lane straight from global memory (r + voff + soff) to LDS
+// (dst + 16 * lane), in assembly: the compiler would hold every LDS read back
+// until all such copies have landed. fence() waits for them.
+__device__ __forceinline__ void copy16(char* dst, u32x4_t r, uint32_t voff, uint32_t soff) {
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_void_t*)dst;
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "{m0}"(at), "v"(voff), "s"(r), "s"(soff)
+               : "memory");
+}
+
+// All but this wave's last N copies have landed and its LDS reads are done;
+// and so it is with every wave of the workgroup.
+template <int N>
+__device__ __forceinline__ void fence() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // One operand's tile of B output rows/columns: copies to LDS and fragment
-// reads. A copy moves 1 KB per wave, straight from global memory to LDS;
-// offsets past the operand's last byte read as 0 and take part in nothing.
+// reads. A copy moves 1 KB per wave; offsets past the operand's last byte read
+// as 0 and take part in nothing.
 //
 // COL false (contiguous along the contraction): B rows of 128 bytes, 16-byte
-// piece c of row r at position c ^ f(r), f = r%8 ^ r/8%2: the 16 rows a
-// fragment read takes one piece from, and any 8 of them side by side, fall on
-// distinct banks.
+// piece c of row r at position c ^ spread(r). A 16-byte LDS read serves lanes
+// 0-3, 12-15, 20-27 at a time, then the others of a half: either way rows of
+// one parity (half of the banks) get eight different positions (no conflict
+// counted).
 // COL true: 64 contraction rows of B values, 32-byte chunk c of row r at
-// c ^ g(r), g = r%4 + 4 (r/8%2); a fragment is two transposing reads of 4
-// rows x 16 values per 16 lanes.
+// c ^ g(r), g = r%4 + 4 (r/8%2) (r%4 in rows of 4 chunks); a fragment is two
+// transposing reads of 4 rows x 16 values per 16 lanes.
+__device__ __forceinline__ int spread(int r) { return ((r >> 1) & 3) | (((r >> 4) & 1) << 2); }
+
 template <int FMT, bool COL, int B, int NW>
 struct Operand {
   static constexpr int kBytes = B * kStageBytes;
@@ -107,15 +146,19 @@ struct Operand {
   static constexpr int kRowB = B * 2;              // COL: bytes of a contraction row
   static constexpr int kLanes = COL ? (kRowB / 16) : 8;   // lanes on one row of a copy
   static constexpr int kRows = 64 / kLanes;        // rows of a copy
-  static_assert(B / 8 % NW == 0 && kRowB <= 1024, "whole copies");
+  static constexpr int kSwz = B >= 128 ? 7 : B / 16 - 1;   // COL: a row's chunks are that many and one more, or twice
+  static constexpr int kTiles = 4;                 // fragments a wave may hold
+  static_assert(B / 8 % NW == 0 && kRowB <= 1024 && (COL || NW % 4 == 0), "whole copies");
 
   const char* base;
   int64_t ld;
-  uint32_t bytes;      // from base to the operand's last byte (COL: of `rows` rows, see at())
+  uint32_t bytes;      // from base to the operand's last byte (COL: of `rows` rows, see copy())
   int rows, width;     // COL: contraction rows, bytes to the last needed column
+                       // else: contraction bytes of a row, and where in a step the lane's piece lies
   uint32_t voff;
-  int rd[COL ? 8 : 2];
+  int rd[4];
 
+  // w0: the wave's first row/column of the tile.
   __device__ __forceinline__ void init(const void* b, int64_t row_bytes, int n, int c_bytes, int wave, int lane,
                                        int w0) {
     base = static_cast<const char*>(b);
@@ -124,56 +167,56 @@ struct Operand {
     if constexpr (COL) {
       rows = n;
       width = c_bytes;
-      const int g = (row & 3) | (((row >> 3) & 1) << 2);
+      const int g = ((row & 3) | (((row >> 3) & 1) << 2)) & kSwz;
       voff = (uint32_t)(row * (int)ld + (((pos >> 1) ^ g) * 2 + (pos & 1)) * 16);
-      const int j = (lane & 15) >> 2, q = lane >> 4, gr = j | ((q & 1) << 2);
+      // 16 lanes read values 16 (l/16%2).. of contraction rows 8 (l/32) + l%16/4
+      const int j = (lane & 15) >> 2, h = lane >> 5, gr = (j | (h << 2)) & kSwz;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) rd[t] = (8 * q + j) * kRowB + (((w0 / 16 + t) ^ gr) * 32) + (lane & 3) * 8;
+      for (int t = 0; t < kTiles; ++t)
+        rd[t] = (8 * h + j) * kRowB + (((w0 / 16 + 2 * t + ((lane >> 4) & 1)) ^ gr) * 32) + (lane & 3) * 8;
     } else {
       bytes = n > 0 ? (uint32_t)((n - 1) * (int)ld + c_bytes) : 0u;
-      const int piece = pos ^ ((row & 7) ^ (wave & 1));
+      const int piece = pos ^ spread(row & 31);
       voff = (uint32_t)(row * (int)ld + piece * 16);
       width = piece * 16;
       rows = c_bytes;
-      const int r = lane & 15, q = lane >> 4, f = (r & 7) ^ (r >> 3);
-      const int first = FMT == FMT_MX ? 2 * q : q, step = FMT == FMT_MX ? 16 : 64;
-      rd[0] = (w0 + r) * kStageBytes + (first ^ f) * 16;
-      rd[1] = rd[0] ^ step;
+      // quarter k of a step: pieces 2k and 2k + 1 of the lane's row; MX: k and k + 4, so that the scales of a lane's
+      // four pieces are one word
+      const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        rd[k] = (w0 + r) * kStageBytes + (((FMT == FMT_MX ? 4 * h + k : 2 * k + h) ^ spread(r)) * 16);
     }
   }
 
-  // Step s into `stage`.
-  __device__ __forceinline__ void copy(char* stage, int s, int wave) const {
+  // Copies [from, to) of this wave's share of step s into `stage`.
+  __device__ __forceinline__ void copy(char* stage, int s, int wave, int from, int to) const {
+    u32x4_t r;
+    uint32_t v = voff, at = 0;
     if constexpr (COL) {
       const int left = min(rows - 64 * s, 64);
-      const __amdgpu_buffer_rsrc_t r =
-          rsrc(base + (int64_t)s * 64 * ld, left > 0 ? (uint32_t)((left - 1) * (int)ld + width) : 0u);
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(stage + (i * NW + wave) * 1024), 16, voff,
-                                                 i * NW * kRows * (int)ld, 0, 0);
+      r = rsrc(base + (int64_t)s * 64 * ld, left > 0 ? (uint32_t)((left - 1) * (int)ld + width) : 0u);
     } else {
-      const __amdgpu_buffer_rsrc_t r = rsrc(base, bytes);
-      const int at = s * kStageBytes;
-      const uint32_t v = at + width < rows ? voff : kPastEnd;   // the row's contraction ends before this piece
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(stage + (i * NW + wave) * 1024), 16, v,
-                                                 i * NW * kRows * (int)ld + at, 0, 0);
+      r = rsrc(base, bytes);
+      at = s * kStageBytes;
+      v = (int)at + width < rows ? voff : kPastEnd;   // or the row's contraction ends before this piece
     }
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      if (i >= from && i < to) copy16(stage + (i * NW + wave) * 1024, r, v, i * NW * kRows * (int)ld + at);
   }
 
-  // Fragment t (16 rows/columns from w0 + 16 t) of half kk of a step.
-  __device__ __forceinline__ u32x4_t frag(const char* stage, int t, int kk) const {
+  // Fragment t (32 rows/columns from w0 + 32 t) of quarter k of a step.
+  __device__ __forceinline__ u32x4_t frag(const char* stage, int t, int k) const {
     if constexpr (COL) {
-      const lds_char_t* at = (const lds_char_t*)(stage + rd[t] + kk * 32 * kRowB);
+      const lds_char_t* at = (const lds_char_t*)(stage + rd[t] + k * 16 * kRowB);
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)at);
       const s16x4_t hi =
           __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(at + 4 * kRowB));
       const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
       return u32x4_t{a[0], a[1], b[0], b[1]};
     } else {
-      return *reinterpret_cast<const u32x4_t*>(stage + rd[kk] + t * 16 * kStageBytes);
+      return *reinterpret_cast<const u32x4_t*>(stage + rd[k] + t * 32 * kStageBytes);
     }
   }
 };
@@ -190,27 +233,262 @@ __device__ __forceinline__ void store4(void* out, int64_t at, int type, f32x4_t 
   }
 }
 
-// One BI x BJ output tile per workgroup of WI x WJ waves. Two LDS stages:
-// while the waves multiply step s, step s + 1 is on its way to the other.
+// Everything of one output tile. BJ may be less than the workgroup's largest
+// tile: a group's last rows.
 template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ>
-__global__ __launch_bounds__(64 * WI * WJ) void ragged_gemm(RaggedParams p) {
-  constexpr int NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
-  constexpr bool MX = FMT == FMT_MX;
-  constexpr int kVal = MX ? 256 : 64;     // contraction values per step
+struct TileBody {
+  static constexpr int NW = WI * WJ, TI = BI / WI / 32, TJ = BJ / WJ / 32;
+  static constexpr bool MX = FMT == FMT_MX;
+  static constexpr int kVal = MX ? 256 : 64;     // contraction values per step
   using OpP = Operand<FMT, PC, BI, NW>;
   using OpQ = Operand<FMT, QC, BJ, NW>;
-  constexpr int kStage = OpP::kBytes + OpQ::kBytes;
-  __shared__ __align__(1024) char lds[2 * kStage];
-  __shared__ __align__(1024) char lds_s[MX ? 2 * (BI + BJ) * 16 : 16];
+  OpP P;
+  OpQ Q;
+  f32x16_t acc[TI][TJ];
+  int wave, lane, wi, wj;
+  int blocks;                       // MX: scale blocks of a row
+  u32x4_t prs, qrs;                 // MX scales
+  int s_ld;
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wi = wave / WJ, wj = wave % WJ;
+  // LDS stages of P and of Q: what fits in 160 KB (MX: with two of scales)
+  static constexpr int kPS = MX ? (BJ > 128 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = MX ? (BJ > 128 ? 2 : 3) : BJ > 128 ? 2 : BJ > 64 ? 3 : 4;
+  static constexpr int kPB = BI * kStageBytes, kQB = BJ * kStageBytes, kSB = MX ? (BI + BJ) * 16 : 0;
+  static constexpr int kPC = OpP::kCopies, kQC = OpQ::kCopies;
+  static constexpr int kLds = kPS * kPB + kQS * kQB + 2 * kSB;
+  static_assert(kLds <= 160 * 1024 && kPS >= kQS, "LDS");
+
+  char* lds;
+  __device__ __forceinline__ char* p_stage(int s) const { return lds + s % kPS * kPB; }
+  __device__ __forceinline__ char* q_stage(int s) const { return lds + kPS * kPB + s % kQS * kQB; }
+  __device__ __forceinline__ char* scales(int s) const {
+    return lds + kPS * kPB + kQS * kQB + ((s >> 1) & 1) * kSB;
+  }
+
+  // MX: the scales of steps s and s + 1, s even.
+  __device__ __forceinline__ void issue_scales(int s) const {
+    char* ss = scales(s);
+#pragma unroll
+    for (int n = 0; n < BI / 64; n += NW)
+      if (n + wave < BI / 64) copy16(ss + (n + wave) * 1024, prs, ((n + wave) * 64 + lane) * s_ld, s * 8);
+#pragma unroll
+    for (int n = 0; n < (BJ + 63) / 64; n += NW)
+      if (n + wave < (BJ + 63) / 64)
+        copy16(ss + BI * 16 + (n + wave) * 1024, qrs, ((n + wave) * 64 + lane) * s_ld, s * 8);
+  }
+
+  // MX: a lane's four scale bytes of step s (its blocks 4h .. 4h + 3) in tile t of P, u of Q.
+  __device__ __forceinline__ int scale(int s, int row) const {
+    return *reinterpret_cast<const int*>(scales(s) + (row + (lane & 31)) * 16 + (s & 1) * 8 + (lane >> 5) * 4);
+  }
+  __device__ __forceinline__ int scale_p(int s, int t) const { return scale(s, wi * (BI / WI) + 32 * t); }
+  __device__ __forceinline__ int scale_q(int s, int u) const { return scale(s, BI + wj * (BJ / WJ) + 32 * u); }
+
+  struct Frags {
+    u32x4_t p[TI], q[TJ];
+  };
+  struct Scales {
+    int p[TI], q[TJ];
+  };
+
+  // Quarter k of a step (stages ps, qs).
+  __device__ __forceinline__ void load(Frags& f, const char* ps, const char* qs, int k) const {
+#pragma unroll
+    for (int t = 0; t < TI; ++t) f.p[t] = P.frag(ps, t, k);
+#pragma unroll
+    for (int u = 0; u < TJ; ++u) f.q[u] = Q.frag(qs, u, k);
+  }
+  __device__ __forceinline__ void load_scales(Scales& c, int s) const {
+#pragma unroll
+    for (int t = 0; t < TI; ++t) c.p[t] = scale_p(s, t);
+#pragma unroll
+    for (int u = 0; u < TJ; ++u) c.q[u] = scale_q(s, u);
+  }
+
+  // Column u of quarter K.
+  template <int K>
+  __device__ __forceinline__ void mul(const Frags& f, const Scales& c, int u) {
+#pragma unroll
+    for (int t = 0; t < TI; ++t) {
+      acc[t][u] = mma<FMT, K>(f.p[t], f.q[u], acc[t][u], c.p[t], c.q[u]);
+      // the compiler would move the scaled products past the branches behind them, and spill their operands
+      if constexpr (MX) asm volatile("" : "+v"(acc[t][u]));
+    }
+  }
+
+  __device__ __forceinline__ void init(const RaggedParams& p, int e, const Group& g, int i0, int j0, int ni, int nj,
+                                       int C) {
+    lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wi = wave / WJ, wj = wave % WJ;
+    constexpr int kBits = MX ? 4 : 16;
+    const char* pb = static_cast<const char*>(p.p);
+    const char* qb = static_cast<const char*>(p.q);
+    const int cb = C / 8 * kBits;   // contraction bytes of a row (C a multiple of 8 there)
+    if constexpr (QC) {
+      P.init(pb + (int64_t)g.lo * p.p_ld + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi * (BI / WI));
+      Q.init(qb + (int64_t)g.lo * p.q_ld + (int64_t)j0 * 2, p.q_ld, C, nj * 2, wave, lane, wj * (BJ / WJ));
+    } else {
+      const char* we = pb + (int64_t)e * p.p_stride;
+      if constexpr (PC)
+        P.init(we + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi * (BI / WI));
+      else
+        P.init(we + (int64_t)i0 * p.p_ld, p.p_ld, ni, cb, wave, lane, wi * (BI / WI));
+      Q.init(qb + (int64_t)(g.lo + j0) * p.q_ld, p.q_ld, nj, cb, wave, lane, wj * (BJ / WJ));
+    }
+    if constexpr (MX) {
+      s_ld = (int)p.s_ld;
+      blocks = C / 32;
+      prs = rsrc(p.ps + (int64_t)e * p.ps_stride + (int64_t)i0 * s_ld, (uint32_t)(ni * s_ld));
+      qrs = rsrc(p.qs + (int64_t)(g.lo + j0) * s_ld, (uint32_t)(nj * s_ld));
+    }
+#pragma unroll
+    for (int t = 0; t < TI; ++t)
+#pragma unroll
+      for (int u = 0; u < TJ; ++u) acc[t][u] = f32x16_t{};
+  }
+
+  // The refills of step s's stages behind its barrier, Q of step s + kQS, then
+  // P of step s + kPS: copy number c of them.
+  template <bool ALL>
+  __device__ __forceinline__ void refill(int s, int c, int steps) const {
+    if (c < kQC) {
+      if (ALL || s + kQS < steps) Q.copy(q_stage(s), s + kQS, wave, c, c + 1);
+    } else if (c < kQC + kPC) {
+      if (ALL || s + kPS < steps) P.copy(p_stage(s), s + kPS, wave, c - kQC, c - kQC + 1);
+    }
+  }
+
+  // The contraction. P and Q pass through rings of LDS stages of one step
+  // each; the fragments of a quarter step are read while the quarter before it
+  // is multiplied. In quarter 3, behind its first columns, comes the one
+  // barrier of a step: every wave's reads of the step's stages are done, and
+  // step s + 1 has landed. The copies that refill the stages follow one by one
+  // between the columns, up to the next step's quarter 2: side by side they
+  // would hold up the products behind them.
+  // The scheduling barriers keep the order as written.
+  //   MODE 0: all refills are within the contraction, 1: some may not be (or s
+  //   is 0), 2: the last step
+  template <int MODE>
+  __device__ __forceinline__ void step(Frags& f, Frags& g, Scales& c, Scales& n, int s, int steps) {
+    constexpr int kHead = TJ > 1 ? TJ / 2 : 1;                              // columns ahead of the barrier
+    constexpr int kGap = (kQC + kPC + 4 * TJ - kHead - 1) / (4 * TJ - kHead);   // copies per column
+    const char* ph = p_stage(s);
+    const char* qh = q_stage(s);
+    if constexpr (MX && MODE == 2) {
+      // scales past the row's last block may hold anything: 2^0 there
+      const int left = blocks - 8 * s - 4 * (lane >> 5);
+      const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left > 0 ? (1u << (8 * left)) - 1u : 0u;
+#pragma unroll
+      for (int t = 0; t < TI; ++t) c.p[t] = (c.p[t] & keep) | (0x7F7F7F7Fu & ~keep);
+#pragma unroll
+      for (int u = 0; u < TJ; ++u) c.q[u] = (c.q[u] & keep) | (0x7F7F7F7Fu & ~keep);
+    }
+    auto column = [&](auto k, Frags& x, int u) {
+      constexpr int K = decltype(k)::value;
+      mul<K>(x, c, u);
+      if constexpr (MODE != 2) {
+        const int at = (K == 3 ? u - kHead : TJ - kHead + K * TJ + u) * kGap;   // the column's place behind a barrier
+#pragma unroll
+        for (int i = 0; i < kGap; ++i) {
+          if (K == 3) refill<MODE == 0>(s, at + i, steps);
+          else if (MODE == 0 || s > 0) refill<MODE == 0>(s - 1, at + i, steps);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    load(g, ph, qh, 1);
+#pragma unroll
+    for (int u = 0; u < TJ; ++u) column(std::integral_constant<int, 0>{}, f, u);
+    load(f, ph, qh, 2);
+#pragma unroll
+    for (int u = 0; u < TJ; ++u) column(std::integral_constant<int, 1>{}, g, u);
+    load(g, ph, qh, 3);
+#pragma unroll
+    for (int u = 0; u < TJ; ++u) column(std::integral_constant<int, 2>{}, f, u);
+#pragma unroll
+    for (int u = 0; u < kHead; ++u) {
+      mul<3>(g, c, u);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (MODE != 2) {
+      // the copies behind those of step s + 1 may still be on their way
+      if (MODE == 0 || s - 1 + kPS < steps) fence<(kQS - 2) * (kPC + kQC) + (kPS > kQS ? kPC : 0)>();
+      else fence<0>();
+      if constexpr (MX) {
+        load_scales(n, s + 1);
+        if (((s + kQS) & 1) == 0 && s + kQS < steps) issue_scales(s + kQS);
+      }
+      load(f, p_stage(s + 1), q_stage(s + 1), 0);
+    }
+#pragma unroll
+    for (int u = kHead; u < TJ; ++u) column(std::integral_constant<int, 3>{}, g, u);
+    if constexpr (MX && MODE != 2) c = n;
+  }
+
+  __device__ __forceinline__ void contract(int steps) {
+    if (steps <= 0) return;
+    Frags f, g;
+    Scales c, n;   // MX: of this step and the next
+#pragma unroll
+    for (int s = 0; s < kPS; ++s) {
+      if constexpr (MX)
+        if ((s & 1) == 0 && s < kQS && s < steps) issue_scales(s);
+      if (s < steps) P.copy(p_stage(s), s, wave, 0, kPC);
+      if (s < kQS && s < steps) Q.copy(q_stage(s), s, wave, 0, kQC);
+    }
+    if (!MX && steps >= kPS) fence<(kPS - 1) * kPC + (kQS - 1) * kQC>();
+    else fence<0>();
+    load(f, p_stage(0), q_stage(0), 0);
+    if constexpr (MX) load_scales(c, 0);
+    int s = 0;
+    if (steps > 1) step<1>(f, g, c, n, s++, steps);
+    for (; s + kPS < steps; ++s) step<0>(f, g, c, n, s, steps);
+    for (; s + 1 < steps; ++s) step<1>(f, g, c, n, s, steps);
+    step<2>(f, g, c, n, s, steps);
+  }
+
+  __device__ __forceinline__ void store(const RaggedParams& p, int64_t base, int64_t row0, int i0, int ni, int nj) {
+#pragma unroll
+    for (int u = 0; u < TJ; ++u) {
+      const int j = wj * (BJ / WJ) + 32 * u + (lane & 31);
+      if (j >= nj) continue;
+#pragma unroll
+      for (int t = 0; t < TI; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = wi * (BI / WI) + 32 * t + 8 * k + 4 * (lane >> 5);
+          const f32x16_t& v = acc[t][u];
+          if (i < ni)
+            store4(p.out, base + (row0 + j) * p.out_ld + i0 + i, p.out_type,
+                   f32x4_t{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]});
+        }
+    }
+  }
+
+  __device__ __forceinline__ static void run(const RaggedParams& p, int e, const Group& g, int i0, int j0, int ni,
+                                             int nj, char* lds) {
+    TileBody b;
+    b.lds = lds;
+    const int C = QC ? g.n : p.C;
+    b.init(p, e, g, i0, j0, ni, nj, C);
+    b.contract((C + kVal - 1) / kVal);
+    b.store(p, QC ? (int64_t)e * p.out_stride : 0, QC ? (int64_t)j0 : (int64_t)(g.lo + j0), i0, ni, nj);
+  }
+};
+
+// One BI x BJ output tile per workgroup of WI x WJ waves.
+template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ>
+__global__ __launch_bounds__(64 * WI * WJ) void ragged_gemm(RaggedParams p) {
+  using Full = TileBody<FMT, PC, QC, BI, BJ, WI, WJ>;
+  using Half = TileBody<FMT, PC, QC, BI, BJ / 2, WI, WJ>;
+  using Quarter = TileBody<FMT, PC, QC, BI, BJ / 4, WI, WJ>;
+  constexpr int kHQ = Half::kLds > Quarter::kLds ? Half::kLds : Quarter::kLds;
+  __shared__ __align__(1024) char lds[Full::kLds > kHQ ? Full::kLds : kHQ];
   const int NI = (p.I + BI - 1) / BI;
-
   int e, it, jt;
   if constexpr (QC) {
     const int nj = (p.J + BJ - 1) / BJ;
-    const int t = xcd_remap(blockIdx.x, gridDim.x);
+    const int t = deal(blockIdx.x, p.E * nj * NI);
+    if (t < 0) return;
     e = t / (nj * NI);
     it = (t - e * nj * NI) / nj;
     jt = t - e * nj * NI - it * nj;
@@ -222,121 +500,20 @@ __global__ __launch_bounds__(64 * WI * WJ) void ragged_gemm(RaggedParams p) {
   const Group g = group_of(p, e);
   const int i0 = it * BI, j0 = jt * BJ;
   const int ni = min(p.I - i0, BI), nj = min((QC ? p.J : g.n) - j0, BJ);
-  const int C = QC ? g.n : p.C;
-
-  OpP P;
-  OpQ Q;
-  constexpr int kBits = MX ? 4 : 16;
-  const char* pb = static_cast<const char*>(p.p);
-  const char* qb = static_cast<const char*>(p.q);
-  const int cb = C / 8 * kBits + C % 8 * kBits / 8;   // contraction bytes of a row
-  if constexpr (QC) {
-    P.init(pb + (int64_t)g.lo * p.p_ld + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi * (BI / WI));
-    Q.init(qb + (int64_t)g.lo * p.q_ld + (int64_t)j0 * 2, p.q_ld, C, nj * 2, wave, lane, wj * (BJ / WJ));
-  } else {
-    const char* we = pb + (int64_t)e * p.p_stride;
-    if constexpr (PC)
-      P.init(we + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi * (BI / WI));
-    else
-      P.init(we + (int64_t)i0 * p.p_ld, p.p_ld, ni, cb, wave, lane, wi * (BI / WI));
-    Q.init(qb + (int64_t)(g.lo + j0) * p.q_ld, p.q_ld, nj, cb, wave, lane, wj * (BJ / WJ));
-  }
-
-  const int steps = (C + kVal - 1) / kVal;
-  const int blocks = C / 32;   // MX: scale blocks of a row
-  auto issue = [&](int s) {
-    char* st = lds + (s & 1) * kStage;
-    P.copy(st, s, wave);
-    Q.copy(st + OpP::kBytes, s, wave);
-    if constexpr (MX) {
-      if ((s & 1) == 0) {
-        // 16 scales of every row: two steps' worth
-        char* ss = lds_s + ((s >> 1) & 1) * (BI + BJ) * 16;
-        const int ld = (int)p.s_ld;
-        for (int n = wave; n < (BI + BJ) / 64; n += NW) {
-          const bool isp = n < BI / 64;
-          const int r0 = (isp ? n : n - BI / 64) * 64;
-          const uint8_t* b = isp ? p.ps + (int64_t)e * p.ps_stride + (int64_t)i0 * ld
-                                 : p.qs + (int64_t)(g.lo + j0) * ld;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(b, (uint32_t)((isp ? ni : nj) * ld)),
-                                                   (lds_void_t*)(ss + n * 1024), 16, (r0 + lane) * ld, s * 8, 0, 0);
-        }
-      }
-    }
-  };
-
-  f32x4_t acc[TI][TJ];
-#pragma unroll
-  for (int t = 0; t < TI; ++t)
-#pragma unroll
-    for (int u = 0; u < TJ; ++u) acc[t][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  if (steps > 0) issue(0);
-  for (int s = 0; s < steps; ++s) {
-    __syncthreads();   // step s has landed, and every wave is past step s - 1
-    if (s + 1 < steps) issue(s + 1);
-    const char* st = lds + (s & 1) * kStage;
-    int sp[TI], sq[TJ];
-    if constexpr (MX) {
-      const char* ss = lds_s + ((s >> 1) & 1) * (BI + BJ) * 16 + (lane & 15) * 16 + (s & 1) * 8 + (lane >> 4) * 2;
-#pragma unroll
-      for (int t = 0; t < TI; ++t)
-        sp[t] = *reinterpret_cast<const uint16_t*>(ss + (wi * (BI / WI) + 16 * t) * 16);
-#pragma unroll
-      for (int u = 0; u < TJ; ++u)
-        sq[u] = *reinterpret_cast<const uint16_t*>(ss + (BI + wj * (BJ / WJ) + 16 * u) * 16);
-      if (8 * s + 8 > blocks) {
-        // scales past the row's last block may hold anything: 2^0 there
-        const int at = 8 * s + 2 * (lane >> 4);
-        const int keep = at + 1 < blocks ? 0xFFFF : at < blocks ? 0xFF : 0;
-#pragma unroll
-        for (int t = 0; t < TI; ++t) sp[t] = (sp[t] & keep) | (0x7F7F & ~keep);
-#pragma unroll
-        for (int u = 0; u < TJ; ++u) sq[u] = (sq[u] & keep) | (0x7F7F & ~keep);
-      }
-    }
-    auto half = [&](auto kk) {
-      constexpr int KK = decltype(kk)::value;
-      u32x4_t pf[TI], qf[TJ];
-#pragma unroll
-      for (int t = 0; t < TI; ++t) pf[t] = P.frag(st, t, KK);
-#pragma unroll
-      for (int u = 0; u < TJ; ++u) qf[u] = Q.frag(st + OpP::kBytes, u, KK);
-#pragma unroll
-      for (int u = 0; u < TJ; ++u)
-#pragma unroll
-        for (int t = 0; t < TI; ++t) {
-          if constexpr (MX) acc[t][u] = mma_mx<KK>(pf[t], qf[u], acc[t][u], sp[t], sq[u]);
-          else acc[t][u] = mma<FMT>(pf[t], qf[u], acc[t][u]);
-        }
-    };
-    half(std::integral_constant<int, 0>{});
-    half(std::integral_constant<int, 1>{});
-  }
-
-  const int64_t row0 = QC ? (int64_t)j0 : (int64_t)(g.lo + j0);
-  const int64_t ob = QC ? (int64_t)e * p.out_stride : 0;
-#pragma unroll
-  for (int u = 0; u < TJ; ++u) {
-    const int j = wj * (BJ / WJ) + 16 * u + (lane & 15);
-    if (j >= nj) continue;
-#pragma unroll
-    for (int t = 0; t < TI; ++t) {
-      const int i = wi * (BI / WI) + 16 * t + 4 * (lane >> 4);
-      if (i < ni) store4(p.out, ob + (row0 + j) * p.out_ld + i0 + i, p.out_type, acc[t][u]);
-    }
-  }
+  if (nj > BJ / 2) Full::run(p, e, g, i0, j0, ni, nj, lds);
+  else if (nj > BJ / 4) Half::run(p, e, g, i0, j0, ni, nj, lds);
+  else Quarter::run(p, e, g, i0, j0, ni, nj, lds);
 }
 
 template <int FMT, bool PC, bool QC>
 hipError_t launch(const RaggedParams& p, hipStream_t s) {
-  constexpr int BI = 128, BJ = 128;
+  constexpr int BI = 256, BJ = 256;
   const int64_t NI = (p.I + BI - 1) / BI;
   const int64_t live = p.E < p.M ? p.E : p.M;   // experts that can hold rows
   const int64_t grid = QC ? p.E * NI * ((p.J + BJ - 1) / BJ) : NI * ((p.M + live * (BJ - 1)) / BJ);
   if (grid == 0) return hipSuccess;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  ragged_gemm<FMT, PC, QC, BI, BJ, 2, 2><<<(unsigned)grid, 256, 0, s>>>(p);
+  if (grid > 0x7FFFFFFF - kDealSlack) return hipErrorInvalidConfiguration;
+  ragged_gemm<FMT, PC, QC, BI, BJ, 4, 2><<<(unsigned)grid + kDealSlack, 512, 0, s>>>(p);
   return hipGetLastError();
 }
 
