@@ -63,12 +63,21 @@ __device__ __forceinline__ int deal(int b, int total) {
 }
 constexpr int kDealSlack = 8 * 32;
 
-// The tile of workgroup b among all experts' tiles of BJ rows x NI columns,
-// experts in order, a column's row tiles side by side. e < 0: none left. Every lane of a wave looks at one of 64
-// experts at a time.
 struct Tile {
   int e, it, jt;
 };
+
+// Tile t of an expert's nj x NI: bands of up to 8 rows, column by column, so
+// that tiles which share weights start side by side and a run of 32 has few
+// operand panels (8 x 4 tiles: 12).
+__device__ __forceinline__ Tile tile_of(int e, int t, int nj, int NI) {
+  const int band = t / (8 * NI), r = t - band * 8 * NI, h = min(8, nj - band * 8);
+  return Tile{e, r / h, band * 8 + r % h};
+}
+
+// The tile of workgroup b among all experts' tiles of BJ rows x NI columns,
+// experts in order. e < 0: none left. Every lane of a wave looks at one of 64
+// experts at a time.
 __device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, int NI) {
   const int lane = threadIdx.x & 63;
   auto count = [&](int e) { return e < p.E ? (group_of(p, e).n + BJ - 1) / BJ : 0; };
@@ -91,9 +100,9 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, 
     if (past) {
       const int at = __builtin_ctzll(past);
       const int ne = __shfl(n, at, 64), local = t - (before + __shfl(sum, at, 64) - ne) * NI;
-      const int it = local / ne;
-      return Tile{__builtin_amdgcn_readfirstlane(base + at), __builtin_amdgcn_readfirstlane(it),
-                  __builtin_amdgcn_readfirstlane(local - it * ne)};
+      const Tile tl = tile_of(base + at, local, ne, NI);
+      return Tile{__builtin_amdgcn_readfirstlane(tl.e), __builtin_amdgcn_readfirstlane(tl.it),
+                  __builtin_amdgcn_readfirstlane(tl.jt)};
     }
     before += __shfl(sum, 63, 64);
   }
@@ -221,15 +230,16 @@ struct Operand {
   }
 };
 
-__device__ __forceinline__ void store4(void* out, int64_t at, int type, f32x4_t v) {
-  if (type == TYPE_BF16) {
-    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + at) =
-        u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  } else if (type == TYPE_F16) {
-    const f16x4_t h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-    *reinterpret_cast<f16x4_t*>(static_cast<_Float16*>(out) + at) = h;
+// Four values rounded to TYPE.
+template <int TYPE>
+__device__ __forceinline__ auto pack4(float a, float b, float c, float d) {
+  if constexpr (TYPE == TYPE_F32) {
+    return f32x4_t{a, b, c, d};
+  } else if constexpr (TYPE == TYPE_F16) {
+    const f16x4_t h = {(_Float16)a, (_Float16)b, (_Float16)c, (_Float16)d};
+    return __builtin_bit_cast(u32x2_t, h);
   } else {
-    *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at) = v;
+    return u32x2_t{pack_bf16x2(a, b), pack_bf16x2(c, d)};
   }
 }
 
@@ -251,7 +261,7 @@ struct TileBody {
   int s_ld;
 
   // LDS stages of P and of Q: what fits in 160 KB (MX: with two of scales)
-  static constexpr int kPS = MX ? (BJ > 128 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = MX ? (BJ > 128 ? 2 : 3) : BJ > 128 ? 2 : BJ > 64 ? 3 : 4;
+  static constexpr int kPS = MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
   static constexpr int kPB = BI * kStageBytes, kQB = BJ * kStageBytes, kSB = MX ? (BI + BJ) * 16 : 0;
   static constexpr int kPC = OpP::kCopies, kQC = OpQ::kCopies;
   static constexpr int kLds = kPS * kPB + kQS * kQB + 2 * kSB;
@@ -446,22 +456,48 @@ struct TileBody {
     step<2>(f, g, c, n, s, steps);
   }
 
-  __device__ __forceinline__ void store(const RaggedParams& p, int64_t base, int64_t row0, int i0, int ni, int nj) {
+  // The tile's rows to global memory, turned in LDS: a lane holds 4 adjacent
+  // values of a row, whole 128-byte lines (16 bytes a lane) go out. In pieces
+  // of 8 bytes the same stores cost 2.4 times as long (weight gradients of 48
+  // experts, 2.8 GB: 885 us of the call).
+  // Each wave turns 32 rows at a time in LDS of its own.
+  template <int TYPE>
+  __device__ __forceinline__ void store_as(const RaggedParams& p, int64_t base, int64_t row0, int i0, int ni, int nj) {
+    constexpr int kW = BI / WI, kSize = TYPE == TYPE_F32 ? 4 : 2;   // columns of a wave
+    constexpr int kRow = kW * kSize, kPitch = kRow + 16;            // 16 bytes more: rows on other banks
+    constexpr int kLanes = kRow / 16, kRows = 64 / kLanes;          // lanes on a row, rows of a store
+    static_assert(NW * 32 * kPitch <= kLds, "LDS");
+    char* buf = lds + wave * 32 * kPitch;
+    const int col = wi * kW + (lane % kLanes) * (16 / kSize);
 #pragma unroll
     for (int u = 0; u < TJ; ++u) {
-      const int j = wj * (BJ / WJ) + 32 * u + (lane & 31);
-      if (j >= nj) continue;
 #pragma unroll
       for (int t = 0; t < TI; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int i = wi * (BI / WI) + 32 * t + 8 * k + 4 * (lane >> 5);
           const f32x16_t& v = acc[t][u];
-          if (i < ni)
-            store4(p.out, base + (row0 + j) * p.out_ld + i0 + i, p.out_type,
-                   f32x4_t{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]});
+          const auto w = pack4<TYPE>(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          __builtin_memcpy(__builtin_assume_aligned(
+                               buf + (lane & 31) * kPitch + (32 * t + 8 * k + 4 * (lane >> 5)) * kSize, 4 * kSize),
+                           &w, sizeof w);
         }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int r = 0; r < 32; r += kRows) {
+        const int j = r + lane / kLanes, jj = wj * (BJ / WJ) + 32 * u + j;
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(buf + j * kPitch + (lane % kLanes) * 16);
+        if (jj < nj && col < ni)
+          *reinterpret_cast<u32x4_t*>(static_cast<char*>(p.out) + (base + (row0 + jj) * p.out_ld + i0 + col) * kSize) = w;
+      }
+      __builtin_amdgcn_wave_barrier();
     }
+  }
+
+  __device__ __forceinline__ void store(const RaggedParams& p, int64_t base, int64_t row0, int i0, int ni, int nj) {
+    fence<0>();   // every wave is past its last fragments
+    if (p.out_type == TYPE_BF16) store_as<TYPE_BF16>(p, base, row0, i0, ni, nj);
+    else if (p.out_type == TYPE_F16) store_as<TYPE_F16>(p, base, row0, i0, ni, nj);
+    else store_as<TYPE_F32>(p, base, row0, i0, ni, nj);
   }
 
   __device__ __forceinline__ static void run(const RaggedParams& p, int e, const Group& g, int i0, int j0, int ni,
@@ -478,11 +514,12 @@ struct TileBody {
 // One BI x BJ output tile per workgroup of WI x WJ waves.
 template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ>
 __global__ __launch_bounds__(64 * WI * WJ) void ragged_gemm(RaggedParams p) {
-  using Full = TileBody<FMT, PC, QC, BI, BJ, WI, WJ>;
-  using Half = TileBody<FMT, PC, QC, BI, BJ / 2, WI, WJ>;
-  using Quarter = TileBody<FMT, PC, QC, BI, BJ / 4, WI, WJ>;
-  constexpr int kHQ = Half::kLds > Quarter::kLds ? Half::kLds : Quarter::kLds;
-  __shared__ __align__(1024) char lds[Full::kLds > kHQ ? Full::kLds : kHQ];
+  using B4 = TileBody<FMT, PC, QC, BI, BJ, WI, WJ>;
+  using B3 = TileBody<FMT, PC, QC, BI, QC ? BJ : BJ / 4 * 3, WI, WJ>;   // (no whole copies of 192 columns)
+  using B2 = TileBody<FMT, PC, QC, BI, BJ / 2, WI, WJ>;
+  using B1 = TileBody<FMT, PC, QC, BI, BJ / 4, WI, WJ>;
+  constexpr auto most = [](int a, int b) { return a > b ? a : b; };
+  __shared__ __align__(1024) char lds[most(most(B4::kLds, B3::kLds), most(B2::kLds, B1::kLds))];
   const int NI = (p.I + BI - 1) / BI;
   int e, it, jt;
   if constexpr (QC) {
@@ -490,8 +527,8 @@ __global__ __launch_bounds__(64 * WI * WJ) void ragged_gemm(RaggedParams p) {
     const int t = deal(blockIdx.x, p.E * nj * NI);
     if (t < 0) return;
     e = t / (nj * NI);
-    it = (t - e * nj * NI) / nj;
-    jt = t - e * nj * NI - it * nj;
+    const Tile tl = tile_of(e, t - e * nj * NI, nj, NI);
+    it = tl.it, jt = tl.jt;
   } else {
     const Tile t = find_tile(p, blockIdx.x, BJ, NI);
     if (t.e < 0) return;
@@ -500,9 +537,11 @@ __global__ __launch_bounds__(64 * WI * WJ) void ragged_gemm(RaggedParams p) {
   const Group g = group_of(p, e);
   const int i0 = it * BI, j0 = jt * BJ;
   const int ni = min(p.I - i0, BI), nj = min((QC ? p.J : g.n) - j0, BJ);
-  if (nj > BJ / 2) Full::run(p, e, g, i0, j0, ni, nj, lds);
-  else if (nj > BJ / 4) Half::run(p, e, g, i0, j0, ni, nj, lds);
-  else Quarter::run(p, e, g, i0, j0, ni, nj, lds);
+  // a group's last rows take a tile of fewer rows: less to multiply, more stages in flight
+  if (QC ? nj > BJ / 2 : nj > BJ / 4 * 3) B4::run(p, e, g, i0, j0, ni, nj, lds);
+  else if (nj > BJ / 2) B3::run(p, e, g, i0, j0, ni, nj, lds);
+  else if (nj > BJ / 4) B2::run(p, e, g, i0, j0, ni, nj, lds);
+  else B1::run(p, e, g, i0, j0, ni, nj, lds);
 }
 
 template <int FMT, bool PC, bool QC>
