@@ -118,6 +118,23 @@ def test_bias_masks_and_ties():
     assert ids.item() == 50
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_order_of_every_kind_of_value(dtype):
+    """Signed zeros are equal (the lower index first), subnormals are not; the largest finite value and infinity."""
+    require_gpu()
+    import w4a16_int4_grouped_amd as M
+    f = torch.finfo(DT[dtype])
+    tiny = f.smallest_normal * f.eps
+    x = torch.tensor([[-0.0, 0.0, -tiny, tiny, 2 * tiny, -2 * tiny, f.max, float("inf"), f.min, -0.0, 1.0, f.max]],
+                     dtype=torch.float64).to(DT[dtype])
+    for shift in range(12):
+        y = torch.roll(x, shift, 1)
+        rid, rw, _ = reference(y, 12, "sigmoid", None, False, 1.0)
+        ids, w = M.router_topk(y.cuda(), 12, "sigmoid")
+        assert torch.equal(ids.cpu().long(), rid), shift
+        assert torch.allclose(w.cpu().double(), rw, rtol=22 * 2.0 ** -24, atol=2.0 ** -126)
+
+
 def test_strided_rows_out_stream_and_guards():
     require_gpu()
     import w4a16_int4_grouped_amd as M

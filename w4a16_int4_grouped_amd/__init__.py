@@ -12,6 +12,7 @@ torch-tensor conveniences.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -371,16 +372,26 @@ def swiglu(h, out=None, stream=None):
 # Operators around the layer
 # ---------------------------------------------------------------------------
 
-_DTYPES = None
+# The smallest of these calls take a few microseconds on the GPU, less than the
+# host needs for a call written carelessly: the helpers below look at every
+# tensor once, pass plain integers to the library and ask torch for the raw
+# stream.
+
+_torch = None
+_CODES = None       # torch dtype -> MOE_DTYPE_*
+
+
+def _load():
+    global _torch, _CODES
+    import torch
+    _CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
+    _torch = torch
+    return torch
 
 
 def _dtype(t) -> int:
     """MOE_DTYPE_* of a torch dtype."""
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
-    code = _DTYPES.get(t)
+    code = _CODES.get(t)
     if code is None:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{t}: bfloat16, float16 or float32")
     return code
@@ -394,32 +405,41 @@ def _need(ok, msg):
 def _matrix(t, name, dtype=None, device=None, shape=None):
     """Checks a tensor's rows: on the GPU (the first operand's), of a dtype
     and shape, values of a row adjacent. Returns the row distance."""
-    _need(t.is_cuda, f"{name}: not on a GPU")
-    _need(device is None or t.device == device, f"{name}: on {t.device}, the first operand on {device}")
-    _need(dtype is None or t.dtype == dtype, f"{name}: {t.dtype}, expected {dtype}")
-    _need(shape is None or tuple(t.shape) == shape, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_cuda:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: not on a GPU")
+    if device is not None and t.device != device:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: on {t.device}, the first operand on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: {t.dtype}, expected {dtype}")
+    s = t.shape
+    if shape is not None and s != shape:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: shape {tuple(s)}, expected {shape}")
+    st = t.stride()
+    width = s[-1]
     # a dimension of one element has no meaningful stride
-    _need(t.stride(-1) == 1 or t.shape[-1] <= 1, f"{name}: the values of a row are not adjacent")
-    rows, width = t.shape[-2], t.shape[-1]
-    return t.stride(-2) if rows > 1 else max(width, (width + 7) // 8 * 8)
+    if st[-1] != 1 and width > 1:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: the values of a row are not adjacent")
+    return st[-2] if s[-2] > 1 else (width + 7) // 8 * 8
 
 
 def _dense(t, name, dtype, device, shape):
-    import torch
-    _need(t.is_cuda and t.device == device, f"{name}: not on the first operand's GPU")
-    _need(t.dtype == dtype, f"{name}: {t.dtype}, expected {dtype}")
-    _need(tuple(t.shape) == shape, f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    _need(t.is_contiguous(), f"{name}: not contiguous")
+    if not t.is_cuda or t.device != device:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: not on the first operand's GPU")
+    if t.dtype != dtype or t.shape != shape:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
+    if not t.is_contiguous():
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: not contiguous")
 
 
 def _call(fn, device, stream, *args):
     """fn(*args, stream) on `device`: on `stream`, or on its current stream."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        check(fn(*args, _stream(stream)))
-    else:
+    torch = _torch
+    if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            check(fn(*args, _stream(stream)))
+            return _call(fn, device, stream, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    if status != MOE_OK:
+        check(status)
 
 
 def router_topk(logits, topk, score="softmax", bias=None, renorm=False, scale=1.0, out=None, stream=None):
@@ -430,12 +450,14 @@ def router_topk(logits, topk, score="softmax", bias=None, renorm=False, scale=1.
     out for the token; places without an expert hold id -1 and weight 0, which
     the layer routes nowhere. logits [T, E] bf16, fp16 or fp32; `out` may give
     the two tensors."""
-    import torch
+    torch = _torch or _load()
     _need(logits.dim() == 2, "logits: [T, E]")
     T, E = logits.shape
     ld = _matrix(logits, "logits")
     dev = logits.device
-    _need(score in SCORES, f"score {score!r}: softmax or sigmoid")
+    if score not in SCORES:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"score {score!r}: softmax or sigmoid")
+    _need(topk >= 1, "topk: at least 1")
     if bias is not None:
         _dense(bias, "bias", torch.float32, dev, (E,))
     if out is None:
@@ -445,8 +467,9 @@ def router_topk(logits, topk, score="softmax", bias=None, renorm=False, scale=1.
         ids, w = out
         _dense(ids, "ids", torch.int32, dev, (T, topk))
         _dense(w, "weights", torch.float32, dev, (T, topk))
-    _call(lib().moe_router_topk, dev, stream, _ptr(logits), _dtype(logits.dtype), max(ld, E), T, E, topk,
-          SCORES[score], _ptr(bias), int(bool(renorm)), float(scale), _ptr(ids), _ptr(w))
+    _call((_lib or lib()).moe_router_topk, dev, stream,
+          logits.data_ptr(), _dtype(logits.dtype), max(ld, E), T, E, topk, SCORES[score],
+          None if bias is None else bias.data_ptr(), 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr())
     return ids, w
 
 
@@ -454,28 +477,30 @@ def router_topk_grad(logits, ids, d_w, score="softmax", renorm=False, scale=1.0,
     """Gradient [T, E] of the logits (their dtype) for the ids that
     router_topk chose with the same score, renorm and scale, and the gradient
     d_w (float32 [T, topk]) of their weights."""
-    import torch
+    torch = _torch or _load()
     _need(logits.dim() == 2 and ids.dim() == 2, "logits: [T, E], ids: [T, topk]")
     T, E = logits.shape
     ld = _matrix(logits, "logits")
     dev = logits.device
     topk = ids.shape[1]
-    _need(score in SCORES, f"score {score!r}: softmax or sigmoid")
+    if score not in SCORES:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"score {score!r}: softmax or sigmoid")
     _dense(ids, "ids", torch.int32, dev, (T, topk))
     _dense(d_w, "d_w", torch.float32, dev, (T, topk))
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=dev)
     o_ld = _matrix(out, "out", logits.dtype, dev, (T, E))
-    _call(lib().moe_router_topk_grad, dev, stream, _ptr(logits), _dtype(logits.dtype), max(ld, E), T, E, topk,
-          SCORES[score], int(bool(renorm)), float(scale), _ptr(ids), _ptr(d_w), _ptr(out), max(o_ld, E))
+    _call((_lib or lib()).moe_router_topk_grad, dev, stream,
+          logits.data_ptr(), _dtype(logits.dtype), max(ld, E), T, E, topk, SCORES[score], 1 if renorm else 0, scale,
+          ids.data_ptr(), d_w.data_ptr(), out.data_ptr(), max(o_ld, E))
     return out
 
 
 def _groups(offsets, device, E=None):
-    import torch
-    _need(offsets.dim() == 1 and offsets.numel() >= 2, "offsets: [E + 1]")
-    E = offsets.numel() - 1 if E is None else E
-    _dense(offsets, "offsets", torch.int32, device, (E + 1,))
+    _need(offsets.dim() == 1 and offsets.shape[0] >= 2, "offsets: [E + 1]")
+    if E is None:
+        E = offsets.shape[0] - 1
+    _dense(offsets, "offsets", _torch.int32, device, (E + 1,))
     return E
 
 
@@ -492,11 +517,12 @@ def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
     not decreasing; out [M, N] of out_dtype (default a's; fp32 as well). Rows
     may be apart (strides of a multiple of 8). Rows of no expert are left as
     they are in `out`. N and K are multiples of 8."""
-    import torch
+    torch = _torch or _load()
     _need(a.dim() == 2 and w.dim() == 3, "a: [M, K], w: [E, N, K]")
     M, K = a.shape
     E, N, Kw = w.shape
-    _need(K == Kw, f"a has {K} columns, w {Kw}")
+    if K != Kw:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"a has {K} columns, w {Kw}")
     dev = a.device
     a_ld = _matrix(a, "a")
     w_ld, w_stride = _weights(w, a.dtype, dev)
@@ -504,18 +530,20 @@ def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype or a.dtype, device=dev)
     o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
-    _call(lib().moe_grouped_gemm, dev, stream, _ptr(a), a_ld, _ptr(w), w_stride, w_ld, _dtype(a.dtype), _ptr(offsets),
-          E, M, N, K, _ptr(out), o_ld, _dtype(out.dtype))
+    _call((_lib or lib()).moe_grouped_gemm, dev, stream,
+          a.data_ptr(), a_ld, w.data_ptr(), w_stride, w_ld, _dtype(a.dtype), offsets.data_ptr(), E, M, N, K,
+          out.data_ptr(), o_ld, _dtype(out.dtype))
     return out
 
 
 def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
     """Gradient of grouped_gemm's `a`: out[r] = dy[r] . w[e], [M, K]."""
-    import torch
+    torch = _torch or _load()
     _need(dy.dim() == 2 and w.dim() == 3, "dy: [M, N], w: [E, N, K]")
     M, N = dy.shape
     E, Nw, K = w.shape
-    _need(N == Nw, f"dy has {N} columns, w {Nw} rows")
+    if N != Nw:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"dy has {N} columns, w {Nw} rows")
     dev = dy.device
     y_ld = _matrix(dy, "dy")
     w_ld, w_stride = _weights(w, dy.dtype, dev)
@@ -523,15 +551,16 @@ def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
     if out is None:
         out = torch.empty((M, K), dtype=out_dtype or dy.dtype, device=dev)
     o_ld = _matrix(out, "out", out_dtype, dev, (M, K))
-    _call(lib().moe_grouped_gemm_dgrad, dev, stream, _ptr(dy), y_ld, _ptr(w), w_stride, w_ld, _dtype(dy.dtype),
-          _ptr(offsets), E, M, N, K, _ptr(out), o_ld, _dtype(out.dtype))
+    _call((_lib or lib()).moe_grouped_gemm_dgrad, dev, stream,
+          dy.data_ptr(), y_ld, w.data_ptr(), w_stride, w_ld, _dtype(dy.dtype), offsets.data_ptr(), E, M, N, K,
+          out.data_ptr(), o_ld, _dtype(out.dtype))
     return out
 
 
 def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
     """Gradient of grouped_gemm's `w`: out[e] = dy[rows of e]^T . a[rows of e],
     [E, N, K]; 0 for an expert without rows."""
-    import torch
+    torch = _torch or _load()
     _need(dy.dim() == 2 and a.dim() == 2 and dy.shape[0] == a.shape[0], "dy: [M, N], a: [M, K]")
     M, N = dy.shape
     K = a.shape[1]
@@ -543,11 +572,13 @@ def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
         out = torch.empty((E, N, K), dtype=out_dtype or dy.dtype, device=dev)
     o_ld = _matrix(out, "out", out_dtype, dev, (E, N, K))
     stride = out.stride(0) if E > 1 else ((N - 1) * o_ld + K + 7) // 8 * 8
-    _call(lib().moe_grouped_gemm_wgrad, dev, stream, _ptr(dy), y_ld, _ptr(a), a_ld, _dtype(dy.dtype), _ptr(offsets),
-          E, M, N, K, _ptr(out), stride, o_ld, _dtype(out.dtype))
+    _call((_lib or lib()).moe_grouped_gemm_wgrad, dev, stream,
+          dy.data_ptr(), y_ld, a.data_ptr(), a_ld, _dtype(dy.dtype), offsets.data_ptr(), E, M, N, K,
+          out.data_ptr(), stride, o_ld, _dtype(out.dtype))
     return out
 
 
+@functools.lru_cache(maxsize=None)
 def mx_scale_cols(K) -> int:
     """Bytes of a row of MXFP4 scales: K / 32 rounded up to a multiple of 16."""
     n = lib().moe_mx_scale_cols(K)
@@ -561,7 +592,7 @@ def mx_quant(x, out=None, stream=None):
     (codes uint8 [..., K/2], the lower nibble first; scales uint8 [...,
     mx_scale_cols(K)], one E8M0 byte per 32 values). More than two dimensions
     must be dense; `out` may give the two tensors."""
-    import torch
+    torch = _torch or _load()
     _need(x.dim() >= 2, "x: [..., K]")
     K = x.shape[-1]
     ld = _matrix(x, "x")
@@ -577,14 +608,14 @@ def mx_quant(x, out=None, stream=None):
         q, scales = out
         _dense(q, "codes", torch.uint8, dev, lead + (K // 2,))
         _dense(scales, "scales", torch.uint8, dev, lead + (cols,))
-    _call(lib().moe_mx_quant, dev, stream, _ptr(x), _dtype(x.dtype), ld if x.dim() == 2 else K, rows, K, _ptr(q),
-          _ptr(scales))
+    _call((_lib or lib()).moe_mx_quant, dev, stream,
+          x.data_ptr(), _dtype(x.dtype), ld if x.dim() == 2 else K, rows, K, q.data_ptr(), scales.data_ptr())
     return q, scales
 
 
 def mx_dequant(q, scales, dtype=None, out=None, stream=None):
     """Values [..., K] of MXFP4 rows in `dtype` (default bf16)."""
-    import torch
+    torch = _torch or _load()
     _need(q.dim() >= 2, "codes: [..., K/2]")
     K = 2 * q.shape[-1]
     lead = tuple(q.shape[:-1])
@@ -595,8 +626,9 @@ def mx_dequant(q, scales, dtype=None, out=None, stream=None):
         out = torch.empty(lead + (K,), dtype=dtype or torch.bfloat16, device=dev)
     ld = _matrix(out, "out", dtype, dev, lead + (K,))
     _need(out.dim() == 2 or out.is_contiguous(), "out: more than two dimensions must be contiguous")
-    _call(lib().moe_mx_dequant, dev, stream, _ptr(q), _ptr(scales), q.numel() * 2 // K, K, _ptr(out),
-          _dtype(out.dtype), ld if out.dim() == 2 else K)
+    _call((_lib or lib()).moe_mx_dequant, dev, stream,
+          q.data_ptr(), scales.data_ptr(), q.numel() * 2 // K, K, out.data_ptr(), _dtype(out.dtype),
+          ld if out.dim() == 2 else K)
     return out
 
 
@@ -604,7 +636,7 @@ def mx_grouped_gemm(aq, a_scales, wq, w_scales, offsets, out=None, out_dtype=Non
     """grouped_gemm on MXFP4 rows (aq uint8 [M, K/2]) and MXFP4 weights (wq
     uint8 [E, N, K/2]) with their scales as mx_quant writes them; out [M, N]
     of out_dtype (default bf16)."""
-    import torch
+    torch = _torch or _load()
     _need(aq.dim() == 2 and wq.dim() == 3, "aq: [M, K/2], wq: [E, N, K/2]")
     M, E, N, K = aq.shape[0], wq.shape[0], wq.shape[1], 2 * aq.shape[1]
     dev = aq.device
@@ -617,8 +649,9 @@ def mx_grouped_gemm(aq, a_scales, wq, w_scales, offsets, out=None, out_dtype=Non
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
     o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
-    _call(lib().moe_mx_grouped_gemm, dev, stream, _ptr(aq), _ptr(a_scales), _ptr(wq), _ptr(w_scales), _ptr(offsets),
-          E, M, N, K, _ptr(out), o_ld, _dtype(out.dtype))
+    _call((_lib or lib()).moe_mx_grouped_gemm, dev, stream,
+          aq.data_ptr(), a_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), E, M, N, K,
+          out.data_ptr(), o_ld, _dtype(out.dtype))
     return out
 
 

@@ -52,24 +52,24 @@ __device__ __forceinline__ Group group_of(const RaggedParams& p, int e) {
 
 // Workgroup b's item of `total`: runs of G consecutive items (tiles that share
 // operands, and one XCD's L2) dealt round-robin to the XCDs, so that each gets
-// its part of large and small experts; -1 past the last. A run is an XCD's 32
-// CUs, less where that would leave XCDs without one. The grid needs total +
-// 8 * 32 workgroups.
+// its part of large and small experts; -1 past the last. A run is 16 items (8,
+// 32 and 64 measured within 3 %), less where that would leave XCDs without
+// one. The grid needs total + 8 * 16 workgroups.
 __device__ __forceinline__ int deal(int b, int total) {
-  const int G = min(max(total / 64, 1), 32);
+  const int G = min(max(total / 64, 1), 16);
   const int idx = b >> 3, run = (idx / G) * 8 + (b & 7);
   const int t = run * G + idx % G;
   return t < total ? t : -1;
 }
-constexpr int kDealSlack = 8 * 32;
+constexpr int kDealSlack = 8 * 16;
 
 struct Tile {
   int e, it, jt;
 };
 
 // Tile t of an expert's nj x NI: bands of up to 8 rows, column by column, so
-// that tiles which share weights start side by side and a run of 32 has few
-// operand panels (8 x 4 tiles: 12).
+// that tiles which share weights start side by side and 32 tiles in a row (an
+// XCD's CUs) have few operand panels (8 x 4: 12).
 __device__ __forceinline__ Tile tile_of(int e, int t, int nj, int NI) {
   const int band = t / (8 * NI), r = t - band * 8 * NI, h = min(8, nj - band * 8);
   return Tile{e, r / h, band * 8 + r % h};
@@ -379,7 +379,7 @@ struct TileBody {
   //   is 0), 2: the last step
   template <int MODE>
   __device__ __forceinline__ void step(Frags& f, Frags& g, Scales& c, Scales& n, int s, int steps) {
-    constexpr int kHead = TJ > 1 ? TJ / 2 : 1;                              // columns ahead of the barrier
+    constexpr int kHead = 1;                                                // columns ahead of the barrier
     constexpr int kGap = (kQC + kPC + 4 * TJ - kHead - 1) / (4 * TJ - kHead);   // copies per column
     const char* ph = p_stage(s);
     const char* qh = q_stage(s);
@@ -487,7 +487,8 @@ struct TileBody {
         const int j = r + lane / kLanes, jj = wj * (BJ / WJ) + 32 * u + j;
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(buf + j * kPitch + (lane % kLanes) * 16);
         if (jj < nj && col < ni)
-          *reinterpret_cast<u32x4_t*>(static_cast<char*>(p.out) + (base + (row0 + jj) * p.out_ld + i0 + col) * kSize) = w;
+          __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(static_cast<char*>(p.out) +
+                                                                   (base + (row0 + jj) * p.out_ld + i0 + col) * kSize));
       }
       __builtin_amdgcn_wave_barrier();
     }

@@ -11,8 +11,12 @@
 // (sigmoid), which neither overflows nor divides by zero.
 //
 // One wave per token: each lane holds the keys of experts lane, lane + 64,
-// ..; a round takes each lane's best, then the wave's. A wave's work is k
-// rounds of dependent lane exchanges, so latency bounds small T.
+// ..; a round takes each lane's best, then the wave's. The k rounds depend on
+// each other, so latency bounds small T: the wave's best comes by six DPP
+// steps (lane exchanges through LDS: 10.4 us for one token of 384 experts
+// with a bias, against 6.7).
+#include <type_traits>
+
 #include "moe_device.h"
 #include "moe_ragged.h"
 
@@ -35,17 +39,54 @@ __device__ __forceinline__ void store1(void* x, int64_t at, float v) {
 
 constexpr float kMax = 3.4028234663852886e38f;
 
-// -inf and NaN become -inf (not chosen), +inf the largest finite value.
-__device__ __forceinline__ float clean(float l) { return l >= -kMax ? fminf(l, kMax) : -INFINITY; }
+// -inf and NaN become -inf (not chosen), +inf the largest finite value, -0 the
+// 0 that it is equal to.
+__device__ __forceinline__ float clean(float l) { return l >= -kMax ? fminf(l, kMax) + 0.f : -INFINITY; }
 
+// v of the lane that DPP control CTRL names; lanes without one keep theirs.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int i = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const int lo = (int)u, hi = (int)(u >> 32);
+  const uint32_t a = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, false);
+  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)b << 32 | a);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)u, 63);
+  const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)b << 32 | a);
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+
+// The largest v of the wave, in every lane (v is no NaN): shifts by 1, 2, 4
+// and 8 lanes within rows of 16, then rows 0 and 2 into 1 and 3, rows 0-1 into
+// 2-3; lane 63 has seen all.
 template <class T>
 __device__ __forceinline__ T wave_max_of(T v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const T u = __shfl_xor(v, o, 64);
-    v = u > v ? u : v;
-  }
-  return v;
+  v = larger(v, dpp<0x111>(v));
+  v = larger(v, dpp<0x112>(v));
+  v = larger(v, dpp<0x114>(v));
+  v = larger(v, dpp<0x118>(v));
+  v = larger(v, dpp<0x142>(v));
+  v = larger(v, dpp<0x143>(v));
+  return last_lane(v);
 }
 template <class T>
 __device__ __forceinline__ T wave_sum_of(T v) {
@@ -68,22 +109,36 @@ __device__ __forceinline__ float chosen_share(float l, int sig) {
   return s > 0.f ? e / s : 0.f;
 }
 
-// VPL: experts per lane. KEY: float (the logits), double (score + bias).
-template <int TYPE, int VPL, class KEY>
+// What a choice is made by.
+//   KEY16  a 16-bit logit's ordered bits above 0xFFFF - expert: one integer
+//          that no other expert has, so the largest names its expert
+//   KEY32  an FP32 logit's ordered bits above 4095 - expert, 44 bits held in a
+//          double (v_max_f64 compares them in one instruction)
+//   KEYB   score + bias in FP64; equal ones are told apart by a ballot
+enum KeyKind : int { KEY16 = 0, KEY32 = 1, KEYB = 2 };
+
+// FP32 bits in the order of their values, and back.
+__device__ __forceinline__ uint32_t ordered(uint32_t b) { return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u); }
+__device__ __forceinline__ uint32_t unordered(uint32_t s) { return s ^ (s >> 31 ? 0x80000000u : 0xFFFFFFFFu); }
+
+// VPL: experts per lane.
+template <int TYPE, int VPL, int KIND>
 __global__ __launch_bounds__(256) void router_topk(RouterParams p) {
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= p.T) return;
   const int64_t row = (int64_t)t * p.ld;
-  float l[VPL];
-  KEY key[VPL];
+  float l[VPL], b[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 64 * i;
-    l[i] = e < p.E ? clean(load1<TYPE>(p.logits, row + e)) : -INFINITY;
+    l[i] = e < p.E ? load1<TYPE>(p.logits, row + e) : -INFINITY;
+    if constexpr (KIND == KEYB) b[i] = e < p.E ? p.bias[e] : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) l[i] = clean(l[i]);
   float top = 0.f, total = 1.f;
-  if (!p.sigmoid && (sizeof(KEY) == 8 || !p.renorm)) {
+  if (!p.sigmoid && (KIND == KEYB || !p.renorm)) {
     top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) top = fmaxf(top, l[i]);
@@ -94,45 +149,96 @@ __global__ __launch_bounds__(256) void router_topk(RouterParams p) {
     for (int i = 0; i < VPL; ++i) total += expf(l[i] - top);
     total = wave_sum_of(total);
   }
-  if constexpr (sizeof(KEY) == 8) {
-    double sum = 1.0;
+  int mine = -1;            // lane j: the j-th choice and its logit
+  float lj = -INFINITY;
+  if constexpr (KIND == KEYB) {
+    double key[VPL], sum = 1.0;
     if (!p.sigmoid) {
       sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += exp((double)l[i] - (double)top);
+      for (int i = 0; i < VPL; ++i)
+        if (64 * i < p.E) sum += exp((double)l[i] - (double)top);
       sum = wave_sum_of(sum);
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 64 * i;
-      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i])) : exp((double)l[i] - (double)top) / sum;
-      const double k = e < p.E ? s + (double)p.bias[e] : 0.0;
-      key[i] = e < p.E && l[i] != -INFINITY && k >= -1.7976931348623157e308 ? k : -INFINITY;
+      key[i] = -INFINITY;
+      if (64 * i < p.E) {
+        const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i])) : exp((double)l[i] - (double)top) / sum;
+        const double k = s + (double)b[i];
+        if (l[i] != -INFINITY && k >= -1.7976931348623157e308) key[i] = k;
+      }
+    }
+    for (int j = 0; j < p.topk; ++j) {
+      double best = key[0];
+      int at = 0;
+#pragma unroll
+      for (int i = 1; i < VPL; ++i)
+        if (key[i] > best) best = key[i], at = i;
+      const double most = wave_max_of(best);
+      if (most == -INFINITY) break;   // the same in every lane: none left
+      const uint64_t has = __ballot(best == most);
+      int owner = __builtin_ctzll(has);
+      if (has & (has - 1)) {
+        // equal keys in several lanes: the lowest expert, so the lowest i, then the lowest lane
+#pragma unroll
+        for (int i = VPL - 1; i >= 0; --i) {
+          const uint64_t m = __ballot(best == most && at == i);
+          if (m) owner = __builtin_ctzll(m);
+        }
+      }
+      float v = l[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) v = at == i ? l[i] : v;
+      const int id = owner + 64 * __builtin_amdgcn_readlane(at, owner);
+      const float lv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), owner));
+      if (lane == j) mine = id, lj = lv;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (id == lane + 64 * i) key[i] = -INFINITY;
     }
   } else {
+    using KEY = std::conditional_t<KIND == KEY16, uint32_t, double>;
+    KEY key[VPL];           // 0: taken or not to be chosen
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = l[i];
-  }
-  int mine = -1;   // lane j: the j-th choice
-  for (int j = 0; j < p.topk; ++j) {
-    KEY best = key[0];
-    int at = lane;
-#pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (key[i] > best) best = key[i], at = lane + 64 * i;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const KEY k = __shfl_xor(best, o, 64);
-      const int a = __shfl_xor(at, o, 64);
-      if (k > best || (k == best && a < at)) best = k, at = a;
+    for (int i = 0; i < VPL; ++i) {
+      const uint32_t e = (uint32_t)(lane + 64 * i);
+      if constexpr (KIND == KEY16) {
+        // the top half of a BF16 logit's FP32 bits, an FP16 logit's own; +inf, above either's largest, as itself
+        const float x = l[i] == kMax ? INFINITY : l[i];
+        uint32_t h;
+        if constexpr (TYPE == TYPE_BF16) h = __float_as_uint(x) >> 16;
+        else h = __builtin_bit_cast(uint16_t, (_Float16)x);
+        h ^= h & 0x8000u ? 0xFFFFu : 0x8000u;
+        key[i] = l[i] == -INFINITY ? 0u : h << 16 | (0xFFFFu - e);
+      } else {
+        const uint64_t k = (uint64_t)ordered(__float_as_uint(l[i])) << 12 | (4095u - e);
+        key[i] = l[i] == -INFINITY ? 0.0 : (double)k;
+      }
     }
-    if (best == -INFINITY) break;   // the same in every lane: none left
-    if (lane == j) mine = at;
+    for (int j = 0; j < p.topk; ++j) {
+      KEY best = key[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (at == lane + 64 * i) key[i] = -INFINITY;
+      for (int i = 1; i < VPL; ++i) best = larger(best, key[i]);
+      const KEY most = wave_max_of(best);
+      if (most == 0) break;   // the same in every lane: none left
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = key[i] == most ? (KEY)0 : key[i];
+      if (lane == j) {
+        if constexpr (KIND == KEY16) {
+          mine = (int)(0xFFFFu - (most & 0xFFFFu));
+          uint32_t h = most >> 16;
+          h ^= h & 0x8000u ? 0x8000u : 0xFFFFu;
+          if constexpr (TYPE == TYPE_BF16) lj = clean(__uint_as_float(h << 16));
+          else lj = clean((float)__builtin_bit_cast(_Float16, (uint16_t)h));
+        } else {
+          const uint64_t k = (uint64_t)most;
+          mine = (int)(4095u - (uint32_t)(k & 4095u));
+          lj = __uint_as_float(unordered((uint32_t)(k >> 12)));
+        }
+      }
+    }
   }
-  const float lj = mine >= 0 ? clean(load1<TYPE>(p.logits, row + mine)) : -INFINITY;
   float w;
   if (p.renorm) w = chosen_share(lj, p.sigmoid);
   else if (mine < 0) w = 0.f;
@@ -151,25 +257,23 @@ __global__ __launch_bounds__(256) void router_topk(RouterParams p) {
 //   sigmoid, renorm   dl_j = u_j (1 - s_j) (g_j - sum g u)
 // and 0 for experts not chosen in the last three. Ids outside [0, E) take no
 // part; an id given twice adds up.
-template <int TYPE>
+// One wave per token; a lane writes V adjacent experts at a time (V = 8, 16
+// bytes and more, where rows allow it; the writes of the dense rows bound the
+// call).
+template <int TYPE, int V>
 __global__ __launch_bounds__(256) void router_topk_grad(RouterParams p) {
-  extern __shared__ float rows[];   // [4][E]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * (blockDim.x >> 6) + wave;
-  const bool live = t < p.T;
-  float* G = rows + wave * p.E;
-  for (int e = lane; e < p.E; e += 64) G[e] = 0.f;
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= p.T) return;
   const int64_t row = (int64_t)t * p.ld;
   int id = -1;
   float lj = -INFINITY, g = 0.f;
-  if (live && lane < p.topk) {
+  if (lane < p.topk) {
     id = p.ids[(int64_t)t * p.topk + lane];
+    g = p.dw[(int64_t)t * p.topk + lane] * p.scale;
     if (id < 0 || id >= p.E) id = -1;
-    if (id >= 0) {
-      lj = clean(load1<TYPE>(p.logits, row + id));
-      g = p.dw[(int64_t)t * p.topk + lane] * p.scale;
-      if (lj == -INFINITY) id = -1, g = 0.f;
-    }
+    if (id >= 0) lj = clean(load1<TYPE>(p.logits, row + id));
+    if (lj == -INFINITY) id = -1, g = 0.f;
   }
   float top = 0.f, total = 1.f, dot = 0.f, d = 0.f;
   const bool dense = !p.sigmoid && !p.renorm;
@@ -183,64 +287,76 @@ __global__ __launch_bounds__(256) void router_topk_grad(RouterParams p) {
   } else {
     d = g;
     top = -INFINITY;
-    if (live)
-      for (int e = lane; e < p.E; e += 64) top = fmaxf(top, clean(load1<TYPE>(p.logits, row + e)));
+    for (int e = lane; e < p.E; e += 64) top = fmaxf(top, clean(load1<TYPE>(p.logits, row + e)));
     top = wave_max_of(top);
     if (top == -INFINITY) top = 0.f;
     total = 0.f;
-    if (live)
-      for (int e = lane; e < p.E; e += 64) total += expf(clean(load1<TYPE>(p.logits, row + e)) - top);
+    for (int e = lane; e < p.E; e += 64) total += expf(clean(load1<TYPE>(p.logits, row + e)) - top);
     total = wave_sum_of(total);
     if (total == 0.f) total = 1.f;
     dot = wave_sum_of(id >= 0 ? g * (expf(lj - top) / total) : 0.f);
   }
-  // the lanes of one id add up in lane order, the first of them writes
-  float sum = 0.f;
-  bool first = id >= 0;
-  for (int j = 0; j < p.topk; ++j) {
-    const int other = __shfl(id, j, 64);
-    const float v = __shfl(d, j, 64);
-    if (other == id) {
-      sum += v;
-      if (j < lane) first = false;
+  for (int e0 = V * lane; e0 < p.E; e0 += 64 * V) {
+    float v[V] = {};
+    for (int j = 0; j < p.topk; ++j) {
+      const int at = __builtin_amdgcn_readlane(id, j) - e0;
+      const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += at == i ? x : 0.f;
     }
-  }
-  __syncthreads();   // zeros of every lane before the chosen entries
-  if (first) G[id] = sum;
-  __syncthreads();
-  if (!live) return;
-  for (int e = lane; e < p.E; e += 64) {
-    float v = G[e];
-    if (dense) v = expf(clean(load1<TYPE>(p.logits, row + e)) - top) / total * (v - dot);
-    store1<TYPE>(p.dlogits, (int64_t)t * p.d_ld + e, v);
+    if (dense) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        v[i] = expf(clean(load1<TYPE>(p.logits, row + e0 + i)) - top) / total * (v[i] - dot);
+    }
+    const int64_t at = (int64_t)t * p.d_ld + e0;
+    if constexpr (V == 1) {
+      store1<TYPE>(p.dlogits, at, v[0]);
+    } else if constexpr (TYPE == TYPE_F32) {
+      f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(p.dlogits) + at);
+      o[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+      o[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (TYPE == TYPE_BF16) {
+          w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        } else {
+          const f16x2_t h = {(_Float16)v[2 * i], (_Float16)v[2 * i + 1]};
+          w[i] = __builtin_bit_cast(uint32_t, h);
+        }
+      }
+      *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.dlogits) + at) = u32x4_t{w[0], w[1], w[2], w[3]};
+    }
   }
 }
 
-template <int TYPE, class KEY>
+template <int TYPE, int KIND>
 hipError_t topk_for(const RouterParams& p, hipStream_t s) {
   const unsigned g = (unsigned)((p.T + 3) / 4);
-  if (p.E <= 64) router_topk<TYPE, 1, KEY><<<g, 256, 0, s>>>(p);
-  else if (p.E <= 256) router_topk<TYPE, 4, KEY><<<g, 256, 0, s>>>(p);
-  else if (p.E <= 512) router_topk<TYPE, 8, KEY><<<g, 256, 0, s>>>(p);
-  else if (p.E <= 1024) router_topk<TYPE, 16, KEY><<<g, 256, 0, s>>>(p);
-  else router_topk<TYPE, 64, KEY><<<g, 256, 0, s>>>(p);
+  if (p.E <= 64) router_topk<TYPE, 1, KIND><<<g, 256, 0, s>>>(p);
+  else if (p.E <= 256) router_topk<TYPE, 4, KIND><<<g, 256, 0, s>>>(p);
+  else if (p.E <= 384) router_topk<TYPE, 6, KIND><<<g, 256, 0, s>>>(p);
+  else if (p.E <= 1024) router_topk<TYPE, 16, KIND><<<g, 256, 0, s>>>(p);
+  else router_topk<TYPE, 64, KIND><<<g, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
 template <int TYPE>
 hipError_t grad_for(const RouterParams& p, hipStream_t s) {
-  // a token's row of FP32 in LDS: 4 tokens a workgroup up to 1024 experts (16 KB), one above
-  const int waves = p.E <= 1024 ? 4 : 1;
-  router_topk_grad<TYPE><<<(unsigned)((p.T + waves - 1) / waves), 64 * waves, (size_t)waves * p.E * 4, s>>>(p);
+  const unsigned g = (unsigned)((p.T + 3) / 4);
+  if (p.E % 8 == 0 && p.d_ld % 8 == 0 && (uintptr_t)p.dlogits % 16 == 0) router_topk_grad<TYPE, 8><<<g, 256, 0, s>>>(p);
+  else router_topk_grad<TYPE, 1><<<g, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_router_topk(const RouterParams& p, int type, hipStream_t s) {
-  if (type == TYPE_BF16) return p.bias ? topk_for<TYPE_BF16, double>(p, s) : topk_for<TYPE_BF16, float>(p, s);
-  if (type == TYPE_F16) return p.bias ? topk_for<TYPE_F16, double>(p, s) : topk_for<TYPE_F16, float>(p, s);
-  return p.bias ? topk_for<TYPE_F32, double>(p, s) : topk_for<TYPE_F32, float>(p, s);
+  if (type == TYPE_BF16) return p.bias ? topk_for<TYPE_BF16, KEYB>(p, s) : topk_for<TYPE_BF16, KEY16>(p, s);
+  if (type == TYPE_F16) return p.bias ? topk_for<TYPE_F16, KEYB>(p, s) : topk_for<TYPE_F16, KEY16>(p, s);
+  return p.bias ? topk_for<TYPE_F32, KEYB>(p, s) : topk_for<TYPE_F32, KEY32>(p, s);
 }
 
 hipError_t launch_router_topk_grad(const RouterParams& p, int type, hipStream_t s) {
