@@ -109,6 +109,15 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, 
   return Tile{-1, 0, 0};
 }
 
+// The same where every expert has J output rows (wgrad), tiles of BJ x BI.
+__device__ __forceinline__ Tile even_tile(const RaggedParams& p, int b, int BJ, int BI) {
+  const int nj = (p.J + BJ - 1) / BJ, NI = (p.I + BI - 1) / BI;
+  const int t = deal(b, p.E * nj * NI);
+  if (t < 0) return Tile{-1, 0, 0};
+  const int e = t / (nj * NI);
+  return tile_of(e, t - e * nj * NI, nj, NI);
+}
+
 // Buffer descriptor of `bytes` bytes from p: loads past the last read 0.
 __device__ __forceinline__ u32x4_t rsrc(const void* p, uint32_t bytes) {
   const uint64_t a = (uint64_t)p;
@@ -157,14 +166,18 @@ struct Operand {
   static constexpr int kRows = 64 / kLanes;        // rows of a copy
   static constexpr int kSwz = B >= 128 ? 7 : B / 16 - 1;   // COL: a row's chunks are that many and one more, or twice
   static constexpr int kTiles = 4;                 // fragments a wave may hold
-  static_assert(B / 8 % NW == 0 && kRowB <= 1024 && (COL || NW % 4 == 0), "whole copies");
+  static_assert(B / 8 % NW == 0 && kRowB <= 1024, "whole copies");
+  // not COL: spread() of a copy's rows changes with 16 rows, so with the copy where fewer than 4 waves share them
+  static constexpr int kVar = COL || NW >= 4 ? 1 : 2;
+  static constexpr int variant(int i) { return kVar == 1 ? 0 : NW == 2 ? i & 1 : (i >> 1) & 1; }
 
   const char* base;
   int64_t ld;
   uint32_t bytes;      // from base to the operand's last byte (COL: of `rows` rows, see copy())
-  int rows, width;     // COL: contraction rows, bytes to the last needed column
-                       // else: contraction bytes of a row, and where in a step the lane's piece lies
-  uint32_t voff;
+  int rows;            // COL: contraction rows; else: contraction bytes of a row
+  int width;           // COL: bytes to the last needed column
+  uint32_t voff[kVar];
+  int piece[kVar];     // not COL: where in a step the lane's piece lies
   int rd[4];
 
   // w0: the wave's first row/column of the tile.
@@ -177,7 +190,7 @@ struct Operand {
       rows = n;
       width = c_bytes;
       const int g = ((row & 3) | (((row >> 3) & 1) << 2)) & kSwz;
-      voff = (uint32_t)(row * (int)ld + (((pos >> 1) ^ g) * 2 + (pos & 1)) * 16);
+      voff[0] = (uint32_t)(row * (int)ld + (((pos >> 1) ^ g) * 2 + (pos & 1)) * 16);
       // 16 lanes read values 16 (l/16%2).. of contraction rows 8 (l/32) + l%16/4
       const int j = (lane & 15) >> 2, h = lane >> 5, gr = (j | (h << 2)) & kSwz;
 #pragma unroll
@@ -185,10 +198,12 @@ struct Operand {
         rd[t] = (8 * h + j) * kRowB + (((w0 / 16 + 2 * t + ((lane >> 4) & 1)) ^ gr) * 32) + (lane & 3) * 8;
     } else {
       bytes = n > 0 ? (uint32_t)((n - 1) * (int)ld + c_bytes) : 0u;
-      const int piece = pos ^ spread(row & 31);
-      voff = (uint32_t)(row * (int)ld + piece * 16);
-      width = piece * 16;
       rows = c_bytes;
+#pragma unroll
+      for (int v = 0; v < kVar; ++v) {
+        piece[v] = (pos ^ spread((row + 16 * v) & 31)) * 16;
+        voff[v] = (uint32_t)(row * (int)ld + piece[v]);
+      }
       // quarter k of a step: pieces 2k and 2k + 1 of the lane's row; MX: k and k + 4, so that the scales of a lane's
       // four pieces are one word
       const int r = lane & 31, h = lane >> 5;
@@ -201,18 +216,21 @@ struct Operand {
   // Copies [from, to) of this wave's share of step s into `stage`.
   __device__ __forceinline__ void copy(char* stage, int s, int wave, int from, int to) const {
     u32x4_t r;
-    uint32_t v = voff, at = 0;
+    uint32_t v[kVar], at = 0;
     if constexpr (COL) {
       const int left = min(rows - 64 * s, 64);
       r = rsrc(base + (int64_t)s * 64 * ld, left > 0 ? (uint32_t)((left - 1) * (int)ld + width) : 0u);
+      v[0] = voff[0];
     } else {
       r = rsrc(base, bytes);
       at = s * kStageBytes;
-      v = (int)at + width < rows ? voff : kPastEnd;   // or the row's contraction ends before this piece
+#pragma unroll
+      for (int k = 0; k < kVar; ++k)   // or the row's contraction ends before this piece
+        v[k] = (int)at + piece[k] < rows ? voff[k] : kPastEnd;
     }
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      if (i >= from && i < to) copy16(stage + (i * NW + wave) * 1024, r, v, i * NW * kRows * (int)ld + at);
+      if (i >= from && i < to) copy16(stage + (i * NW + wave) * 1024, r, v[variant(i)], i * NW * kRows * (int)ld + at);
   }
 
   // Fragment t (32 rows/columns from w0 + 32 t) of quarter k of a step.
@@ -230,6 +248,24 @@ struct Operand {
   }
 };
 
+// The operands of the tile at (i0, j0) of expert e; wi0, wj0: the wave's part of it.
+template <int FMT, bool PC, bool QC, class OpP, class OpQ>
+__device__ __forceinline__ void init_operands(OpP& P, OpQ& Q, const RaggedParams& p, int e, const Group& g, int i0,
+                                              int j0, int ni, int nj, int C, int wave, int lane, int wi0, int wj0) {
+  const char* pb = static_cast<const char*>(p.p);
+  const char* qb = static_cast<const char*>(p.q);
+  const int cb = C / 8 * (FMT == FMT_MX ? 4 : 16);   // contraction bytes of a row (C a multiple of 8 there)
+  if constexpr (QC) {
+    P.init(pb + (int64_t)g.lo * p.p_ld + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi0);
+    Q.init(qb + (int64_t)g.lo * p.q_ld + (int64_t)j0 * 2, p.q_ld, C, nj * 2, wave, lane, wj0);
+  } else {
+    const char* we = pb + (int64_t)e * p.p_stride;
+    if constexpr (PC) P.init(we + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi0);
+    else P.init(we + (int64_t)i0 * p.p_ld, p.p_ld, ni, cb, wave, lane, wi0);
+    Q.init(qb + (int64_t)(g.lo + j0) * p.q_ld, p.q_ld, nj, cb, wave, lane, wj0);
+  }
+}
+
 // Four values rounded to TYPE.
 template <int TYPE>
 __device__ __forceinline__ auto pack4(float a, float b, float c, float d) {
@@ -241,6 +277,15 @@ __device__ __forceinline__ auto pack4(float a, float b, float c, float d) {
   } else {
     return u32x2_t{pack_bf16x2(a, b), pack_bf16x2(c, d)};
   }
+}
+
+__device__ __forceinline__ void store4(void* out, int64_t at, int type, f32x4_t v) {
+  if (type == TYPE_BF16)
+    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + at) = pack4<TYPE_BF16>(v[0], v[1], v[2], v[3]);
+  else if (type == TYPE_F16)
+    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + at) = pack4<TYPE_F16>(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at) = v;
 }
 
 // Everything of one output tile. BJ may be less than the workgroup's largest
@@ -260,8 +305,9 @@ struct TileBody {
   u32x4_t prs, qrs;                 // MX scales
   int s_ld;
 
-  // LDS stages of P and of Q: what fits in 160 KB (MX: with two of scales)
-  static constexpr int kPS = MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
+  // LDS stages of P and of Q: for 8 waves what fits in 160 KB (MX: with two of scales), for 4 two of each, so that two
+  // workgroups share a CU
+  static constexpr int kPS = NW == 4 ? 2 : MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = NW == 4 || BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
   static constexpr int kPB = BI * kStageBytes, kQB = BJ * kStageBytes, kSB = MX ? (BI + BJ) * 16 : 0;
   static constexpr int kPC = OpP::kCopies, kQC = OpQ::kCopies;
   static constexpr int kLds = kPS * kPB + kQS * kQB + 2 * kSB;
@@ -329,21 +375,7 @@ struct TileBody {
                                        int C) {
     lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wi = wave / WJ, wj = wave % WJ;
-    constexpr int kBits = MX ? 4 : 16;
-    const char* pb = static_cast<const char*>(p.p);
-    const char* qb = static_cast<const char*>(p.q);
-    const int cb = C / 8 * kBits;   // contraction bytes of a row (C a multiple of 8 there)
-    if constexpr (QC) {
-      P.init(pb + (int64_t)g.lo * p.p_ld + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi * (BI / WI));
-      Q.init(qb + (int64_t)g.lo * p.q_ld + (int64_t)j0 * 2, p.q_ld, C, nj * 2, wave, lane, wj * (BJ / WJ));
-    } else {
-      const char* we = pb + (int64_t)e * p.p_stride;
-      if constexpr (PC)
-        P.init(we + (int64_t)i0 * 2, p.p_ld, C, ni * 2, wave, lane, wi * (BI / WI));
-      else
-        P.init(we + (int64_t)i0 * p.p_ld, p.p_ld, ni, cb, wave, lane, wi * (BI / WI));
-      Q.init(qb + (int64_t)(g.lo + j0) * p.q_ld, p.q_ld, nj, cb, wave, lane, wj * (BJ / WJ));
-    }
+    init_operands<FMT, PC, QC>(P, Q, p, e, g, i0, j0, ni, nj, C, wave, lane, wi * (BI / WI), wj * (BJ / WJ));
     if constexpr (MX) {
       s_ld = (int)p.s_ld;
       blocks = C / 32;
@@ -514,46 +546,214 @@ struct TileBody {
 
 // One BI x BJ output tile per workgroup of WI x WJ waves.
 template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ>
-__global__ __launch_bounds__(64 * WI * WJ) void ragged_gemm(RaggedParams p) {
+__global__ __launch_bounds__(64 * WI * WJ) __attribute__((amdgpu_waves_per_eu(2, 2))) void ragged_gemm(RaggedParams p) {
+  constexpr bool kLarge = WI * WJ == 8;
   using B4 = TileBody<FMT, PC, QC, BI, BJ, WI, WJ>;
-  using B3 = TileBody<FMT, PC, QC, BI, QC ? BJ : BJ / 4 * 3, WI, WJ>;   // (no whole copies of 192 columns)
+  using B3 = TileBody<FMT, PC, QC, BI, kLarge && !QC ? BJ / 4 * 3 : BJ, WI, WJ>;   // (no whole copies otherwise)
   using B2 = TileBody<FMT, PC, QC, BI, BJ / 2, WI, WJ>;
-  using B1 = TileBody<FMT, PC, QC, BI, BJ / 4, WI, WJ>;
+  using B1 = TileBody<FMT, PC, QC, BI, BJ / 4, kLarge ? WI : WI * 2, kLarge ? WJ : WJ / 2>;
   constexpr auto most = [](int a, int b) { return a > b ? a : b; };
   __shared__ __align__(1024) char lds[most(most(B4::kLds, B3::kLds), most(B2::kLds, B1::kLds))];
-  const int NI = (p.I + BI - 1) / BI;
-  int e, it, jt;
-  if constexpr (QC) {
-    const int nj = (p.J + BJ - 1) / BJ;
-    const int t = deal(blockIdx.x, p.E * nj * NI);
-    if (t < 0) return;
-    e = t / (nj * NI);
-    const Tile tl = tile_of(e, t - e * nj * NI, nj, NI);
-    it = tl.it, jt = tl.jt;
-  } else {
-    const Tile t = find_tile(p, blockIdx.x, BJ, NI);
-    if (t.e < 0) return;
-    e = t.e, it = t.it, jt = t.jt;
-  }
+  const Tile t = QC ? even_tile(p, blockIdx.x, BJ, BI) : find_tile(p, blockIdx.x, BJ, (p.I + BI - 1) / BI);
+  if (t.e < 0) return;
+  const int e = t.e;
   const Group g = group_of(p, e);
-  const int i0 = it * BI, j0 = jt * BJ;
+  const int i0 = t.it * BI, j0 = t.jt * BJ;
   const int ni = min(p.I - i0, BI), nj = min((QC ? p.J : g.n) - j0, BJ);
+  if (i0 < 0 || j0 < 0 || ni <= 0 || nj <= 0) return;   // sums of offsets that decrease may wrap
   // a group's last rows take a tile of fewer rows: less to multiply, more stages in flight
-  if (QC ? nj > BJ / 2 : nj > BJ / 4 * 3) B4::run(p, e, g, i0, j0, ni, nj, lds);
-  else if (nj > BJ / 2) B3::run(p, e, g, i0, j0, ni, nj, lds);
+  if (nj > (kLarge && !QC ? BJ / 4 * 3 : BJ / 2)) B4::run(p, e, g, i0, j0, ni, nj, lds);
+  else if (kLarge && !QC && nj > BJ / 2) B3::run(p, e, g, i0, j0, ni, nj, lds);
   else if (nj > BJ / 4) B2::run(p, e, g, i0, j0, ni, nj, lds);
   else B1::run(p, e, g, i0, j0, ni, nj, lds);
 }
 
+// One 64 x BJ tile of four waves that share its contraction: wave w takes steps
+// w, w + 4, .. on stages of its own, without a barrier, and the four FP32 sums
+// are added in wave order through LDS. For calls of few tiles, where a tile's
+// chain of steps is the time.
+template <int FMT, bool PC, bool QC, int BJ>
+struct SplitBody {
+  static constexpr int BI = 64, W = 4, TI = 2, TJ = BJ / 32;
+  static constexpr bool MX = FMT == FMT_MX;
+  static constexpr int kVal = MX ? 256 : 64;
+  using OpP = Operand<FMT, PC, BI, 1>;
+  using OpQ = Operand<FMT, QC, BJ, 1>;
+  static constexpr int kSB = MX ? 2048 : 0;                        // 16 scales of up to 128 rows
+  static constexpr int kStage = (BI + BJ) * kStageBytes + kSB;
+  static constexpr int kCopies = OpP::kCopies + OpQ::kCopies + (MX ? 2 : 0);
+  static constexpr int kPitch = BI * 4 + 16, kSum = BJ * kPitch;   // a wave's sums
+  static constexpr int kLds = W * (2 * kStage > kSum ? 2 * kStage : kSum);
+  static_assert(kLds <= 160 * 1024, "LDS");
+
+  __device__ __forceinline__ static void run(const RaggedParams& p, int e, const Group& g, int i0, int j0, int ni,
+                                             int nj, char* all) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char* lds = all + wave * (kLds / W);
+    const int C = QC ? g.n : p.C, steps = (C + kVal - 1) / kVal, blocks = C / 32;
+    const int mine = steps > wave ? (steps - wave + W - 1) / W : 0;
+    OpP P;
+    OpQ Q;
+    init_operands<FMT, PC, QC>(P, Q, p, e, g, i0, j0, ni, nj, C, 0, lane, 0, 0);
+    u32x4_t prs, qrs;
+    if constexpr (MX) {
+      prs = rsrc(p.ps + (int64_t)e * p.ps_stride + (int64_t)i0 * p.s_ld, (uint32_t)(ni * (int)p.s_ld));
+      qrs = rsrc(p.qs + (int64_t)(g.lo + j0) * p.s_ld, (uint32_t)(nj * (int)p.s_ld));
+    }
+    auto issue = [&](int k) {
+      char* st = lds + (k & 1) * kStage;
+      const int s = k * W + wave;
+      P.copy(st, s, 0, 0, OpP::kCopies);
+      Q.copy(st + OpP::kBytes, s, 0, 0, OpQ::kCopies);
+      if constexpr (MX) {
+        char* ss = st + OpP::kBytes + OpQ::kBytes;
+        copy16(ss, prs, lane * (int)p.s_ld, (s & ~1) * 8);
+        copy16(ss + 1024, qrs, lane * (int)p.s_ld, (s & ~1) * 8);
+      }
+    };
+    f32x16_t acc[TI][TJ];
+#pragma unroll
+    for (int t = 0; t < TI; ++t)
+#pragma unroll
+      for (int u = 0; u < TJ; ++u) acc[t][u] = f32x16_t{};
+    if (mine > 0) issue(0);
+    if (mine > 1) issue(1);
+    for (int k = 0; k < mine; ++k) {
+      if (k + 1 < mine) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const char* st = lds + (k & 1) * kStage;
+      const int s = k * W + wave;
+      int sp[TI] = {}, sq[TJ] = {};
+      if constexpr (MX) {
+        const char* ss = st + OpP::kBytes + OpQ::kBytes + (lane & 31) * 16 + (s & 1) * 8 + (lane >> 5) * 4;
+        // scales past the row's last block may hold anything: 2^0 there
+        const int left = blocks - 8 * s - 4 * (lane >> 5);
+        const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left > 0 ? (1u << (8 * left)) - 1u : 0u;
+        auto get = [&](int row) {
+          return (int)((*reinterpret_cast<const uint32_t*>(ss + row * 16) & keep) | (0x7F7F7F7Fu & ~keep));
+        };
+#pragma unroll
+        for (int t = 0; t < TI; ++t) sp[t] = get(32 * t);
+#pragma unroll
+        for (int u = 0; u < TJ; ++u) sq[u] = get(64 + 32 * u);
+      }
+      auto quarter = [&](auto kk) {
+        constexpr int K = decltype(kk)::value;
+        u32x4_t pf[TI], qf[TJ];
+#pragma unroll
+        for (int t = 0; t < TI; ++t) pf[t] = P.frag(st, t, K);
+#pragma unroll
+        for (int u = 0; u < TJ; ++u) qf[u] = Q.frag(st + OpP::kBytes, u, K);
+#pragma unroll
+        for (int t = 0; t < TI; ++t)
+#pragma unroll
+          for (int u = 0; u < TJ; ++u) acc[t][u] = mma<FMT, K>(pf[t], qf[u], acc[t][u], sp[t], sq[u]);
+      };
+      quarter(std::integral_constant<int, 0>{});
+      quarter(std::integral_constant<int, 1>{});
+      quarter(std::integral_constant<int, 2>{});
+      quarter(std::integral_constant<int, 3>{});
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read
+      if (k + 2 < mine) issue(k + 2);
+    }
+    // the sums as rows j of 64 values i
+#pragma unroll
+    for (int u = 0; u < TJ; ++u)
+#pragma unroll
+      for (int t = 0; t < TI; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f32x16_t& v = acc[t][u];
+          *reinterpret_cast<f32x4_t*>(lds + (32 * u + (lane & 31)) * kPitch + (32 * t + 8 * k + 4 * (lane >> 5)) * 4) =
+              f32x4_t{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+        }
+    __syncthreads();
+    const int64_t at = QC ? (int64_t)e * p.out_stride + (int64_t)j0 * p.out_ld : (int64_t)(g.lo + j0) * p.out_ld;
+    const int i = (lane & 15) * 4;
+#pragma unroll
+    for (int r = 0; r < BJ / W; r += 4) {
+      const int j = wave * (BJ / W) + r + (lane >> 4);
+      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += *reinterpret_cast<const f32x4_t*>(all + w * (kLds / W) + j * kPitch + i * 4);
+      if (j < nj && i < ni) store4(p.out, at + (int64_t)j * p.out_ld + i0 + i, p.out_type, v);
+    }
+  }
+};
+
+template <int FMT, bool PC, bool QC>
+__global__ __launch_bounds__(256) void ragged_split(RaggedParams p) {
+  using Wide = SplitBody<FMT, PC, QC, 64>;
+  using Narrow = SplitBody<FMT, PC, QC, 32>;
+  __shared__ __align__(1024) char lds[Wide::kLds > Narrow::kLds ? Wide::kLds : Narrow::kLds];
+  const Tile t = QC ? even_tile(p, blockIdx.x, 64, 64) : find_tile(p, blockIdx.x, 64, (p.I + 63) / 64);
+  if (t.e < 0) return;
+  const Group g = group_of(p, t.e);
+  const int i0 = t.it * 64, j0 = t.jt * 64;
+  const int ni = min(p.I - i0, 64), nj = min((QC ? p.J : g.n) - j0, 64);
+  if (i0 < 0 || j0 < 0 || ni <= 0 || nj <= 0) return;   // as above
+  if (nj > 32) Wide::run(p, t.e, g, i0, j0, ni, nj, lds);
+  else Narrow::run(p, t.e, g, i0, j0, ni, nj, lds);
+}
+
+// Tiles of B x B: at most, where groups are ragged.
+template <bool QC>
+int64_t tile_bound(const RaggedParams& p, int B) {
+  const int64_t NI = (p.I + B - 1) / B, live = p.E < p.M ? p.E : p.M;   // experts that can hold rows
+  return QC ? p.E * NI * ((p.J + B - 1) / B) : NI * ((p.M + live * (B - 1)) / B);
+}
+
+// Which tiles a call takes, by what a call of each would take. Measured on
+// products of 1 to 48 experts, in us:
+//   256 x 256, 8 waves, a workgroup per CU:  a step 1.0 (few workgroups) to 1.75 (all CUs busy), less with fewer rows
+//                                            (a group's last tile), 10 a tile besides
+//   128 x 128, 4 waves, two a CU:            0.65 to 1.0, 5 besides
+//   64 x 64, the contraction split over 4 waves: 0.75 for four steps, 4 besides
+// in as many rounds as the CUs need, and no less than the bytes at 5.5 TB/s.
+// E.g. (N, K, rows of one expert) 512, 7168, 512: 115 / 77 / 25; 4096, 4096,
+// 1024: 75 / 47 / 60; 48 experts of 4096, 7168 and 512 rows: 1180 against 1400
+// for the second. Ties (the bytes) go to the largest.
+struct Estimate {
+  double us[3];
+};
+template <int FMT, bool QC>
+Estimate estimate(const RaggedParams& p) {
+  const double live = p.E < p.M ? p.E : p.M, rows = p.M / live;
+  const double C = QC ? rows : p.C;
+  const double steps = __builtin_ceil(C / (FMT == FMT_MX ? 256 : 64));
+  auto tiles = [&](int B) {
+    return (QC ? p.E * __builtin_ceil((double)p.J / B) : live * __builtin_ceil(rows / B)) *
+           __builtin_ceil((double)p.I / B);
+  };
+  auto busy = [](double n, double full) { return n < full ? n / full : 1.0; };
+  const double j = QC ? p.J : rows;   // rows of an expert's tiles
+  const double part = j <= 64 ? 0.5 : j <= 128 ? 0.65 : j <= 192 ? 0.83 : 1.0;
+  const double size = FMT == FMT_MX ? 17.0 / 32 : 2;
+  const double bytes = QC ? (double)p.M * (p.I + p.J) * 2 + (double)p.E * p.I * p.J * (p.out_type == TYPE_F32 ? 4 : 2)
+                          : live * p.I * p.C * size + (double)p.M * (p.C * size + p.I * (p.out_type == TYPE_F32 ? 4 : 2));
+  const double n0 = tiles(256), n1 = tiles(128), n2 = tiles(64);
+  Estimate e{{__builtin_ceil(n0 / 256) * (steps * (1.0 + 0.75 * busy(n0, 256)) * part + 10),
+              __builtin_ceil(n1 / 512) * (steps * (0.65 + 0.35 * busy(n1, 512)) * (j <= 64 ? 0.75 : 1.0) + 5),
+              __builtin_ceil(n2 / 256) * (__builtin_ceil(steps / 4) * 0.75 + 4)}};
+  for (double& us : e.us) us = us > bytes / 5.5e6 ? us : bytes / 5.5e6;
+  return e;
+}
+
 template <int FMT, bool PC, bool QC>
 hipError_t launch(const RaggedParams& p, hipStream_t s) {
-  constexpr int BI = 256, BJ = 256;
-  const int64_t NI = (p.I + BI - 1) / BI;
-  const int64_t live = p.E < p.M ? p.E : p.M;   // experts that can hold rows
-  const int64_t grid = QC ? p.E * NI * ((p.J + BJ - 1) / BJ) : NI * ((p.M + live * (BJ - 1)) / BJ);
-  if (grid == 0) return hipSuccess;
+  if (!QC && p.M == 0) return hipSuccess;
+  int pick = 0;
+  if (p.M > 0) {
+    const Estimate e = estimate<FMT, QC>(p);
+    if (e.us[1] < e.us[pick]) pick = 1;
+    if (e.us[2] < e.us[pick]) pick = 2;
+  }
+  const int64_t grid = tile_bound<QC>(p, 256 >> pick);
   if (grid > 0x7FFFFFFF - kDealSlack) return hipErrorInvalidConfiguration;
-  ragged_gemm<FMT, PC, QC, BI, BJ, 4, 2><<<(unsigned)grid + kDealSlack, 512, 0, s>>>(p);
+  const unsigned n = (unsigned)grid + kDealSlack;
+  if (pick == 0) ragged_gemm<FMT, PC, QC, 256, 256, 4, 2><<<n, 512, 0, s>>>(p);
+  else if (pick == 1) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2><<<n, 256, 0, s>>>(p);
+  else ragged_split<FMT, PC, QC><<<n, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
