@@ -112,7 +112,8 @@ SHAPES = [
 
 
 def operands(E, N, K, rows, seed):
-    """Random codes and scales near 2^0: on multiples of 2^-6 of at most 72 * 8, so FP32 sums are exact."""
+    """Random codes and scales of 2^-2 .. 2^1: products are multiples of 2^-6 of either sign and at most 144, whose FP32
+    sums over these lengths stay exact (below 2^24 such steps)."""
     g = torch.Generator().manual_seed(seed)
     aq = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, generator=g)
     wq = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, generator=g)

@@ -290,7 +290,9 @@ __device__ __forceinline__ void store4(void* out, int64_t at, int type, f32x4_t 
 
 // Everything of one output tile. BJ may be less than the workgroup's largest
 // tile: a group's last rows.
-template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ>
+// ONE: a single LDS stage, no overlap within a workgroup (four of them share a
+// CU): for contractions of about a step.
+template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ, bool ONE>
 struct TileBody {
   static constexpr int NW = WI * WJ, TI = BI / WI / 32, TJ = BJ / WJ / 32;
   static constexpr bool MX = FMT == FMT_MX;
@@ -307,10 +309,11 @@ struct TileBody {
 
   // LDS stages of P and of Q: for 8 waves what fits in 160 KB (MX: with two of scales), for 4 two of each, so that two
   // workgroups share a CU
-  static constexpr int kPS = NW == 4 ? 2 : MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = NW == 4 || BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
+  static constexpr int kPS = ONE ? 1 : NW == 4 ? 2 : MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = ONE ? 1 : NW == 4 || BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
   static constexpr int kPB = BI * kStageBytes, kQB = BJ * kStageBytes, kSB = MX ? (BI + BJ) * 16 : 0;
   static constexpr int kPC = OpP::kCopies, kQC = OpQ::kCopies;
-  static constexpr int kLds = kPS * kPB + kQS * kQB + 2 * kSB;
+  static constexpr int kTurn = NW * 32 * (BI / WI * 4 + 16);   // what store() needs for FP32
+  static constexpr int kRings = kPS * kPB + kQS * kQB + 2 * kSB, kLds = kRings > kTurn ? kRings : kTurn;
   static_assert(kLds <= 160 * 1024 && kPS >= kQS, "LDS");
 
   char* lds;
@@ -358,6 +361,16 @@ struct TileBody {
     for (int t = 0; t < TI; ++t) c.p[t] = scale_p(s, t);
 #pragma unroll
     for (int u = 0; u < TJ; ++u) c.q[u] = scale_q(s, u);
+  }
+
+  // Scales past the row's last block may hold anything: 2^0 there.
+  __device__ __forceinline__ void cut_scales(Scales& c, int s) const {
+    const int left = blocks - 8 * s - 4 * (lane >> 5);
+    const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left > 0 ? (1u << (8 * left)) - 1u : 0u;
+#pragma unroll
+    for (int t = 0; t < TI; ++t) c.p[t] = (c.p[t] & keep) | (0x7F7F7F7Fu & ~keep);
+#pragma unroll
+    for (int u = 0; u < TJ; ++u) c.q[u] = (c.q[u] & keep) | (0x7F7F7F7Fu & ~keep);
   }
 
   // Column u of quarter K.
@@ -415,15 +428,7 @@ struct TileBody {
     constexpr int kGap = (kQC + kPC + 4 * TJ - kHead - 1) / (4 * TJ - kHead);   // copies per column
     const char* ph = p_stage(s);
     const char* qh = q_stage(s);
-    if constexpr (MX && MODE == 2) {
-      // scales past the row's last block may hold anything: 2^0 there
-      const int left = blocks - 8 * s - 4 * (lane >> 5);
-      const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left > 0 ? (1u << (8 * left)) - 1u : 0u;
-#pragma unroll
-      for (int t = 0; t < TI; ++t) c.p[t] = (c.p[t] & keep) | (0x7F7F7F7Fu & ~keep);
-#pragma unroll
-      for (int u = 0; u < TJ; ++u) c.q[u] = (c.q[u] & keep) | (0x7F7F7F7Fu & ~keep);
-    }
+    if constexpr (MX && MODE == 2) cut_scales(c, s);
     auto column = [&](auto k, Frags& x, int u) {
       constexpr int K = decltype(k)::value;
       mul<K>(x, c, u);
@@ -464,6 +469,35 @@ struct TileBody {
 #pragma unroll
     for (int u = kHead; u < TJ; ++u) column(std::integral_constant<int, 3>{}, g, u);
     if constexpr (MX && MODE != 2) c = n;
+  }
+
+  __device__ __forceinline__ void contract_one(int steps) {
+    Frags f, g;
+    Scales c;
+    for (int s = 0; s < steps; ++s) {
+      if (s > 0) fence<0>();   // every wave's reads of step s - 1 are done
+      if constexpr (MX)
+        if ((s & 1) == 0) issue_scales(s);
+      P.copy(p_stage(s), s, wave, 0, kPC);
+      Q.copy(q_stage(s), s, wave, 0, kQC);
+      fence<0>();
+      load(f, p_stage(s), q_stage(s), 0);
+      if constexpr (MX) {
+        load_scales(c, s);
+        if (s + 1 == steps) cut_scales(c, s);
+      }
+      load(g, p_stage(s), q_stage(s), 1);
+#pragma unroll
+      for (int u = 0; u < TJ; ++u) mul<0>(f, c, u);
+      load(f, p_stage(s), q_stage(s), 2);
+#pragma unroll
+      for (int u = 0; u < TJ; ++u) mul<1>(g, c, u);
+      load(g, p_stage(s), q_stage(s), 3);
+#pragma unroll
+      for (int u = 0; u < TJ; ++u) mul<2>(f, c, u);
+#pragma unroll
+      for (int u = 0; u < TJ; ++u) mul<3>(g, c, u);
+    }
   }
 
   __device__ __forceinline__ void contract(int steps) {
@@ -539,19 +573,21 @@ struct TileBody {
     b.lds = lds;
     const int C = QC ? g.n : p.C;
     b.init(p, e, g, i0, j0, ni, nj, C);
-    b.contract((C + kVal - 1) / kVal);
+    if constexpr (ONE) b.contract_one((C + kVal - 1) / kVal);
+    else b.contract((C + kVal - 1) / kVal);
     b.store(p, QC ? (int64_t)e * p.out_stride : 0, QC ? (int64_t)j0 : (int64_t)(g.lo + j0), i0, ni, nj);
   }
 };
 
 // One BI x BJ output tile per workgroup of WI x WJ waves.
-template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ>
-__global__ __launch_bounds__(64 * WI * WJ) __attribute__((amdgpu_waves_per_eu(2, 2))) void ragged_gemm(RaggedParams p) {
-  constexpr bool kLarge = WI * WJ == 8;
-  using B4 = TileBody<FMT, PC, QC, BI, BJ, WI, WJ>;
-  using B3 = TileBody<FMT, PC, QC, BI, kLarge && !QC ? BJ / 4 * 3 : BJ, WI, WJ>;   // (no whole copies otherwise)
-  using B2 = TileBody<FMT, PC, QC, BI, BJ / 2, WI, WJ>;
-  using B1 = TileBody<FMT, PC, QC, BI, BJ / 4, kLarge ? WI : WI * 2, kLarge ? WJ : WJ / 2>;
+template <int FMT, bool PC, bool QC, int BI, int BJ, int WI, int WJ, bool ONE>
+__global__ __launch_bounds__(64 * WI * WJ)
+__attribute__((amdgpu_waves_per_eu(ONE ? 4 : 2, ONE ? 4 : 2))) void ragged_gemm(RaggedParams p) {
+  constexpr bool kLarge = BJ == 256, kThree = kLarge && !QC;   // (otherwise no whole copies, or no whole fragments)
+  using B4 = TileBody<FMT, PC, QC, BI, BJ, WI, WJ, ONE>;
+  using B3 = TileBody<FMT, PC, QC, BI, kThree ? BJ / 4 * 3 : BJ, WI, WJ, ONE>;
+  using B2 = TileBody<FMT, PC, QC, BI, BJ / 2, WI, WJ, ONE>;
+  using B1 = TileBody<FMT, PC, QC, BI, BJ / 4, kLarge ? WI : WI * 2, kLarge ? WJ : WJ / 2, ONE>;
   constexpr auto most = [](int a, int b) { return a > b ? a : b; };
   __shared__ __align__(1024) char lds[most(most(B4::kLds, B3::kLds), most(B2::kLds, B1::kLds))];
   const Tile t = QC ? even_tile(p, blockIdx.x, BJ, BI) : find_tile(p, blockIdx.x, BJ, (p.I + BI - 1) / BI);
@@ -562,8 +598,8 @@ __global__ __launch_bounds__(64 * WI * WJ) __attribute__((amdgpu_waves_per_eu(2,
   const int ni = min(p.I - i0, BI), nj = min((QC ? p.J : g.n) - j0, BJ);
   if (i0 < 0 || j0 < 0 || ni <= 0 || nj <= 0) return;   // sums of offsets that decrease may wrap
   // a group's last rows take a tile of fewer rows: less to multiply, more stages in flight
-  if (nj > (kLarge && !QC ? BJ / 4 * 3 : BJ / 2)) B4::run(p, e, g, i0, j0, ni, nj, lds);
-  else if (kLarge && !QC && nj > BJ / 2) B3::run(p, e, g, i0, j0, ni, nj, lds);
+  if (nj > (kThree ? BJ / 4 * 3 : BJ / 2)) B4::run(p, e, g, i0, j0, ni, nj, lds);
+  else if (kThree && nj > BJ / 2) B3::run(p, e, g, i0, j0, ni, nj, lds);
   else if (nj > BJ / 4) B2::run(p, e, g, i0, j0, ni, nj, lds);
   else B1::run(p, e, g, i0, j0, ni, nj, lds);
 }
@@ -703,21 +739,27 @@ int64_t tile_bound(const RaggedParams& p, int B) {
   return QC ? p.E * NI * ((p.J + B - 1) / B) : NI * ((p.M + live * (B - 1)) / B);
 }
 
-// Which tiles a call takes, by what a call of each would take. Measured on
-// products of 1 to 48 experts, in us:
-//   256 x 256, 8 waves, a workgroup per CU:  a step 1.0 (few workgroups) to 1.75 (all CUs busy), less with fewer rows
-//                                            (a group's last tile), 10 a tile besides
-//   128 x 128, 4 waves, two a CU:            0.65 to 1.0, 5 besides
-//   64 x 64, the contraction split over 4 waves: 0.75 for four steps, 4 besides
-// in as many rounds as the CUs need, and no less than the bytes at 5.5 TB/s.
-// E.g. (N, K, rows of one expert) 512, 7168, 512: 115 / 77 / 25; 4096, 4096,
-// 1024: 75 / 47 / 60; 48 experts of 4096, 7168 and 512 rows: 1180 against 1400
-// for the second. Ties (the bytes) go to the largest.
-struct Estimate {
-  double us[3];
-};
+// The forms of tiles, and which a call takes: the one whose estimate is the
+// least. An estimate is rounds of workgroups times the us of one, and no less
+// than the bytes at 5.5 TB/s; ties (the bytes) go to the first.
+//   LARGE  256 x 256, 8 waves, a workgroup per CU: a step (64 values, 256 in FP4) 1.0 alone to 1.75 on all CUs, less
+//          where a group's last tile has fewer rows, 10 besides
+//   TWO    128 x 128, 4 waves, two a CU: 0.65 to 1.0 a step, 5 besides
+//   FOUR   the same in one LDS stage, four a CU that cover for each other: 0.95 to 2.0, 6 besides (14 where output
+//          rows do not begin on 128-byte lines: twice the writes)
+//   SPLIT  64 x 64, the contraction split over 4 waves: 0.75 for four steps, 4 besides
+// Measured in us (rows in all, N, K):       LARGE   TWO  FOUR SPLIT
+//   48 experts, 24576, 4096, 7168            1467          2327
+//   384 experts, 32768, 7168, 256             517   514   409  2070
+//   16 experts, 8192, 2048, 1024               52    47    48   107
+//   1 expert, 1024, 4096, 4096                 74    47    68    59
+//   1 expert, 512, 512, 7168                  113    76   110    25
+//   wgrad, 64 experts, 4000, 2048, 2048       134   130   107   717
+enum Form : int { LARGE = 0, TWO = 1, FOUR = 2, SPLIT = 3 };
+
 template <int FMT, bool QC>
-Estimate estimate(const RaggedParams& p) {
+Form form_of(const RaggedParams& p) {
+  if (p.M == 0) return LARGE;
   const double live = p.E < p.M ? p.E : p.M, rows = p.M / live;
   const double C = QC ? rows : p.C;
   const double steps = __builtin_ceil(C / (FMT == FMT_MX ? 256 : 64));
@@ -727,32 +769,36 @@ Estimate estimate(const RaggedParams& p) {
   };
   auto busy = [](double n, double full) { return n < full ? n / full : 1.0; };
   const double j = QC ? p.J : rows;   // rows of an expert's tiles
-  const double part = j <= 64 ? 0.5 : j <= 128 ? 0.65 : j <= 192 ? 0.83 : 1.0;
-  const double size = FMT == FMT_MX ? 17.0 / 32 : 2;
-  const double bytes = QC ? (double)p.M * (p.I + p.J) * 2 + (double)p.E * p.I * p.J * (p.out_type == TYPE_F32 ? 4 : 2)
-                          : live * p.I * p.C * size + (double)p.M * (p.C * size + p.I * (p.out_type == TYPE_F32 ? 4 : 2));
+  const double part = j <= 64 ? 0.5 : j <= 128 ? 0.65 : j <= 192 ? 0.83 : 1.0, few = j <= 64 ? 0.75 : 1.0;
+  const double size = FMT == FMT_MX ? 17.0 / 32 : 2, osize = p.out_type == TYPE_F32 ? 4 : 2;
+  const double bytes = QC ? (double)p.M * (p.I + p.J) * 2 + (double)p.E * p.I * p.J * osize
+                          : live * p.I * p.C * size + (double)p.M * (p.C * size + p.I * osize);
   const double n0 = tiles(256), n1 = tiles(128), n2 = tiles(64);
-  Estimate e{{__builtin_ceil(n0 / 256) * (steps * (1.0 + 0.75 * busy(n0, 256)) * part + 10),
-              __builtin_ceil(n1 / 512) * (steps * (0.65 + 0.35 * busy(n1, 512)) * (j <= 64 ? 0.75 : 1.0) + 5),
-              __builtin_ceil(n2 / 256) * (__builtin_ceil(steps / 4) * 0.75 + 4)}};
-  for (double& us : e.us) us = us > bytes / 5.5e6 ? us : bytes / 5.5e6;
-  return e;
+  const bool lines = p.out_ld * (int64_t)osize % 128 == 0;
+  const double us[4] = {
+      __builtin_ceil(n0 / 256) * (steps * (1.0 + 0.75 * busy(n0, 256)) * part + 10),
+      __builtin_ceil(n1 / 512) * (steps * (0.65 + 0.35 * busy(n1, 512)) * few + 5),
+      __builtin_ceil(n1 / 1024) * (steps * (0.95 + 1.05 * busy(n1, 1024)) * few + (lines ? 6 : 14)),
+      __builtin_ceil(n2 / 256) * (__builtin_ceil(steps / 4) * 0.75 + 4)};
+  int best = LARGE;
+  double least = 0;
+  for (int f = LARGE; f <= SPLIT; ++f) {
+    const double t = us[f] > bytes / 5.5e6 ? us[f] : bytes / 5.5e6;
+    if (f == LARGE || t < least) best = f, least = t;
+  }
+  return (Form)best;
 }
 
 template <int FMT, bool PC, bool QC>
 hipError_t launch(const RaggedParams& p, hipStream_t s) {
   if (!QC && p.M == 0) return hipSuccess;
-  int pick = 0;
-  if (p.M > 0) {
-    const Estimate e = estimate<FMT, QC>(p);
-    if (e.us[1] < e.us[pick]) pick = 1;
-    if (e.us[2] < e.us[pick]) pick = 2;
-  }
-  const int64_t grid = tile_bound<QC>(p, 256 >> pick);
+  const Form f = form_of<FMT, QC>(p);
+  const int64_t grid = tile_bound<QC>(p, f == LARGE ? 256 : f == SPLIT ? 64 : 128);
   if (grid > 0x7FFFFFFF - kDealSlack) return hipErrorInvalidConfiguration;
   const unsigned n = (unsigned)grid + kDealSlack;
-  if (pick == 0) ragged_gemm<FMT, PC, QC, 256, 256, 4, 2><<<n, 512, 0, s>>>(p);
-  else if (pick == 1) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2><<<n, 256, 0, s>>>(p);
+  if (f == LARGE) ragged_gemm<FMT, PC, QC, 256, 256, 4, 2, false><<<n, 512, 0, s>>>(p);
+  else if (f == TWO) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, false><<<n, 256, 0, s>>>(p);
+  else if (f == FOUR) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, true><<<n, 256, 0, s>>>(p);
   else ragged_split<FMT, PC, QC><<<n, 256, 0, s>>>(p);
   return hipGetLastError();
 }
