@@ -431,6 +431,14 @@ def _dense(t, name, dtype, device, shape):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: not contiguous")
 
 
+def _new(shape, dtype, device, stream):
+    """An output; on a stream other than the current one, kept from reuse until that stream is done with it."""
+    t = _torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _call(fn, device, stream, *args):
     """fn(*args, stream) on `device`: on `stream`, or on its current stream."""
     torch = _torch
@@ -461,8 +469,8 @@ def router_topk(logits, topk, score="softmax", bias=None, renorm=False, scale=1.
     if bias is not None:
         _dense(bias, "bias", torch.float32, dev, (E,))
     if out is None:
-        ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
-        w = torch.empty((T, topk), dtype=torch.float32, device=dev)
+        ids = _new((T, topk), torch.int32, dev, stream)
+        w = _new((T, topk), torch.float32, dev, stream)
     else:
         ids, w = out
         _dense(ids, "ids", torch.int32, dev, (T, topk))
@@ -488,7 +496,7 @@ def router_topk_grad(logits, ids, d_w, score="softmax", renorm=False, scale=1.0,
     _dense(ids, "ids", torch.int32, dev, (T, topk))
     _dense(d_w, "d_w", torch.float32, dev, (T, topk))
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        out = _new((T, E), logits.dtype, dev, stream)
     o_ld = _matrix(out, "out", logits.dtype, dev, (T, E))
     _call((_lib or lib()).moe_router_topk_grad, dev, stream,
           logits.data_ptr(), _dtype(logits.dtype), max(ld, E), T, E, topk, SCORES[score], 1 if renorm else 0, scale,
@@ -517,7 +525,8 @@ def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
     not decreasing; out [M, N] of out_dtype (default a's; fp32 as well). Rows
     may be apart (strides of a multiple of 8). Rows of no expert are left as
     they are in `out`. N and K are multiples of 8."""
-    torch = _torch or _load()
+    if _torch is None:
+        _load()
     _need(a.dim() == 2 and w.dim() == 3, "a: [M, K], w: [E, N, K]")
     M, K = a.shape
     E, N, Kw = w.shape
@@ -528,7 +537,7 @@ def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
     w_ld, w_stride = _weights(w, a.dtype, dev)
     _groups(offsets, dev, E)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or a.dtype, device=dev)
+        out = _new((M, N), out_dtype or a.dtype, dev, stream)
     o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
     _call((_lib or lib()).moe_grouped_gemm, dev, stream,
           a.data_ptr(), a_ld, w.data_ptr(), w_stride, w_ld, _dtype(a.dtype), offsets.data_ptr(), E, M, N, K,
@@ -538,7 +547,8 @@ def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
 
 def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
     """Gradient of grouped_gemm's `a`: out[r] = dy[r] . w[e], [M, K]."""
-    torch = _torch or _load()
+    if _torch is None:
+        _load()
     _need(dy.dim() == 2 and w.dim() == 3, "dy: [M, N], w: [E, N, K]")
     M, N = dy.shape
     E, Nw, K = w.shape
@@ -549,7 +559,7 @@ def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
     w_ld, w_stride = _weights(w, dy.dtype, dev)
     _groups(offsets, dev, E)
     if out is None:
-        out = torch.empty((M, K), dtype=out_dtype or dy.dtype, device=dev)
+        out = _new((M, K), out_dtype or dy.dtype, dev, stream)
     o_ld = _matrix(out, "out", out_dtype, dev, (M, K))
     _call((_lib or lib()).moe_grouped_gemm_dgrad, dev, stream,
           dy.data_ptr(), y_ld, w.data_ptr(), w_stride, w_ld, _dtype(dy.dtype), offsets.data_ptr(), E, M, N, K,
@@ -560,7 +570,8 @@ def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
 def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
     """Gradient of grouped_gemm's `w`: out[e] = dy[rows of e]^T . a[rows of e],
     [E, N, K]; 0 for an expert without rows."""
-    torch = _torch or _load()
+    if _torch is None:
+        _load()
     _need(dy.dim() == 2 and a.dim() == 2 and dy.shape[0] == a.shape[0], "dy: [M, N], a: [M, K]")
     M, N = dy.shape
     K = a.shape[1]
@@ -569,7 +580,7 @@ def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
     a_ld = _matrix(a, "a", dy.dtype, dev)
     E = _groups(offsets, dev)
     if out is None:
-        out = torch.empty((E, N, K), dtype=out_dtype or dy.dtype, device=dev)
+        out = _new((E, N, K), out_dtype or dy.dtype, dev, stream)
     o_ld = _matrix(out, "out", out_dtype, dev, (E, N, K))
     stride = out.stride(0) if E > 1 else ((N - 1) * o_ld + K + 7) // 8 * 8
     _call((_lib or lib()).moe_grouped_gemm_wgrad, dev, stream,
@@ -602,8 +613,8 @@ def mx_quant(x, out=None, stream=None):
     dev = x.device
     lead = tuple(x.shape[:-1])
     if out is None:
-        q = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=dev)
-        scales = torch.empty(lead + (cols,), dtype=torch.uint8, device=dev)
+        q = _new(lead + (K // 2,), torch.uint8, dev, stream)
+        scales = _new(lead + (cols,), torch.uint8, dev, stream)
     else:
         q, scales = out
         _dense(q, "codes", torch.uint8, dev, lead + (K // 2,))
@@ -623,7 +634,7 @@ def mx_dequant(q, scales, dtype=None, out=None, stream=None):
     _dense(q, "codes", torch.uint8, dev, tuple(q.shape))
     _dense(scales, "scales", torch.uint8, dev, lead + (mx_scale_cols(K),))
     if out is None:
-        out = torch.empty(lead + (K,), dtype=dtype or torch.bfloat16, device=dev)
+        out = _new(lead + (K,), dtype or torch.bfloat16, dev, stream)
     ld = _matrix(out, "out", dtype, dev, lead + (K,))
     _need(out.dim() == 2 or out.is_contiguous(), "out: more than two dimensions must be contiguous")
     _call((_lib or lib()).moe_mx_dequant, dev, stream,
@@ -647,7 +658,7 @@ def mx_grouped_gemm(aq, a_scales, wq, w_scales, offsets, out=None, out_dtype=Non
     _dense(w_scales, "w_scales", torch.uint8, dev, (E, N, cols))
     _groups(offsets, dev, E)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = _new((M, N), out_dtype or torch.bfloat16, dev, stream)
     o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
     _call((_lib or lib()).moe_mx_grouped_gemm, dev, stream,
           aq.data_ptr(), a_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), E, M, N, K,

@@ -75,38 +75,55 @@ __device__ __forceinline__ Tile tile_of(int e, int t, int nj, int NI) {
   return Tile{e, r / h, band * 8 + r % h};
 }
 
-// The tile of workgroup b among all experts' tiles of BJ rows x NI columns,
-// experts in order. e < 0: none left. Every lane of a wave looks at one of 64
-// experts at a time.
-__device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, int NI) {
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive
   const int lane = threadIdx.x & 63;
-  auto count = [&](int e) { return e < p.E ? (group_of(p, e).n + BJ - 1) / BJ : 0; };
-  int total = 0;
-  for (int base = 0; base < p.E; base += 64) total += count(base + lane);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
-  const int t = deal(b, __builtin_amdgcn_readfirstlane(total) * NI);
-  if (t < 0) return Tile{-1, 0, 0};
-  int before = 0;
-  for (int base = 0; base < p.E; base += 64) {
-    const int n = count(base + lane);
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(sum, o, 64);
-      sum += lane >= o ? v : 0;
-    }
-    const uint64_t past = __ballot((before + sum) * NI > t);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      const int ne = __shfl(n, at, 64), local = t - (before + __shfl(sum, at, 64) - ne) * NI;
-      const Tile tl = tile_of(base + at, local, ne, NI);
-      return Tile{__builtin_amdgcn_readfirstlane(tl.e), __builtin_amdgcn_readfirstlane(tl.it),
-                  __builtin_amdgcn_readfirstlane(tl.jt)};
-    }
-    before += __shfl(sum, 63, 64);
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    v += lane >= o ? u : 0;
   }
-  return Tile{-1, 0, 0};
+  return v;
+}
+
+// The tile of workgroup b among all experts' tiles of BJ rows x NI columns,
+// experts in order. e < 0: none left. A lane adds up the tiles of ceil(E / 64)
+// neighbouring experts, a scan finds the lane that holds the tile, and with an
+// expert of that lane's per lane a second scan the expert: three loads one
+// after the other, whatever E.
+__device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, int NI) {
+  const int lane = threadIdx.x & 63, each = (p.E + 63) / 64;
+  const int32_t* off = p.offsets;
+  int mine = 0;
+  {
+    int e = lane * each;
+    const int end = min(e + each, p.E);
+    int lo = e < end ? off[e] : 0;
+#pragma unroll 8
+    for (; e < end; ++e) {
+      const int hi = off[e + 1];
+      const int from = min(max(lo, 0), p.M);
+      mine += (min(max(hi, from), p.M) - from + BJ - 1) / BJ;
+      lo = hi;
+    }
+  }
+  int sum = wave_scan(mine);
+  const int t = deal(b, __builtin_amdgcn_readlane(sum, 63) * NI);
+  if (t < 0) return Tile{-1, 0, 0};
+  uint64_t past = __ballot(sum * NI > t);
+  if (!past) return Tile{-1, 0, 0};
+  int at = __builtin_ctzll(past);
+  const int before = __builtin_amdgcn_readlane(sum - mine, at), e0 = at * each;
+  const int e = e0 + lane;
+  const int n = lane < each && e < p.E ? (group_of(p, e).n + BJ - 1) / BJ : 0;
+  sum = wave_scan(n);
+  past = __ballot((before + sum) * NI > t);
+  if (!past) return Tile{-1, 0, 0};
+  at = __builtin_ctzll(past);
+  const int ne = __builtin_amdgcn_readlane(n, at);
+  const int local = t - (before + __builtin_amdgcn_readlane(sum, at) - ne) * NI;
+  const Tile tl = tile_of(e0 + at, local, ne, NI);
+  return Tile{__builtin_amdgcn_readfirstlane(tl.e), __builtin_amdgcn_readfirstlane(tl.it),
+              __builtin_amdgcn_readfirstlane(tl.jt)};
 }
 
 // The same where every expert has J output rows (wgrad), tiles of BJ x BI.
