@@ -31,7 +31,8 @@ __device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
   } else {
-    const u32x4_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(x) + at));
+    const u32x4_t w =
+        __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(x) + at));
     if constexpr (TYPE == TYPE_BF16) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);

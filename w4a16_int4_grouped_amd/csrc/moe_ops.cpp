@@ -28,7 +28,8 @@ moe_status_t check_matrix(const char* name, const void* p, int64_t ld, int64_t w
 moe_status_t check_router(const void* logits, int dtype, int64_t ld, int T, int E, int topk, int score) {
   if (!type_ok(dtype)) return fail(MOE_ERR_INVALID_ARG, "dtype = %d", dtype);
   if (E < 1 || E > kMaxExperts) return fail(MOE_ERR_INVALID_ARG, "E = %d outside 1..%d", E, kMaxExperts);
-  if (T < 0 || T > kMaxRows / kMaxTopk) return fail(MOE_ERR_INVALID_ARG, "T = %d outside 0..%d", T, kMaxRows / kMaxTopk);
+  if (T < 0 || T > kMaxRows / kMaxTopk)
+    return fail(MOE_ERR_INVALID_ARG, "T = %d outside 0..%d", T, kMaxRows / kMaxTopk);
   if (topk < 1 || topk > E || topk > kMaxTopk)
     return fail(MOE_ERR_INVALID_ARG, "topk = %d outside 1..min(E, %d)", topk, kMaxTopk);
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return fail(MOE_ERR_INVALID_ARG, "score = %d", score);
@@ -156,9 +157,10 @@ moe_status_t moe_grouped_gemm_wgrad(const void* dy, int64_t dy_ld, const void* a
                                     int64_t dw_stride, int64_t dw_ld, int32_t out_dtype, moe_stream_t stream) {
   moe_status_t st = check_groups(dtype, offsets, E, M, N, K, out_dtype, 8);
   if (st != MOE_OK) return st;
-  if ((M > 0 && ((st = check_matrix("dy", dy, dy_ld, N)) != MOE_OK || (st = check_matrix("a", a, a_ld, K)) != MOE_OK)) ||
-      (st = check_matrix("dw", dw, dw_ld, K)) != MOE_OK)
+  if (M > 0 &&
+      ((st = check_matrix("dy", dy, dy_ld, N)) != MOE_OK || (st = check_matrix("a", a, a_ld, K)) != MOE_OK))
     return st;
+  if ((st = check_matrix("dw", dw, dw_ld, K)) != MOE_OK) return st;
   if (dw_stride % 8 || dw_stride < (int64_t)(N - 1) * dw_ld + K)
     return fail(MOE_ERR_INVALID_ARG, "dw: experts overlap, or are not a multiple of 8 values apart");
   RaggedParams p{};
@@ -185,8 +187,9 @@ moe_status_t moe_mx_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows
   if (st != MOE_OK) return st;
   if (rows == 0) return ok();
   const hipStream_t s = (hipStream_t)stream;
-  return launched(run("mx_quant", s, [&] { return launch_mx_quant(x, dtype, rows, K, ld, q, scales, scale_cols(K), s); }),
-                  "MXFP4 quantisation launch");
+  return launched(
+      run("mx_quant", s, [&] { return launch_mx_quant(x, dtype, rows, K, ld, q, scales, scale_cols(K), s); }),
+      "MXFP4 quantisation launch");
 }
 
 moe_status_t moe_mx_dequant(const uint8_t* q, const uint8_t* scales, int64_t rows, int32_t K, void* out, int32_t dtype,
