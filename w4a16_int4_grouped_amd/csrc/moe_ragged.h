@@ -33,6 +33,7 @@ struct RaggedParams {
   void* out;
   int64_t out_ld, out_stride;    // elements; wgrad: from expert to expert
   int out_type;
+  int stream_out;         // set by the launcher: the output passes the caches by
 };
 
 // type: of both operands (bf16 / f16), ignored for WAY_MX.

@@ -188,8 +188,10 @@ __device__ __forceinline__ void fence() {
 // one parity (half of the banks) get eight different positions (no conflict
 // counted).
 // COL true: 64 contraction rows of B values, 32-byte chunk c of row r at
-// c ^ g(r), g = r%4 + 4 (r/8%2) (r%4 in rows of 4 chunks); a fragment is two
-// transposing reads of 4 rows x 16 values per 16 lanes.
+// c ^ chunk_swizzle(r); a fragment is two transposing reads of 4 rows x 16
+// values per 16 lanes. 32 lanes are served at a time: two neighbouring chunks
+// of 4 rows in a row, whose 8 places must fall on all banks (c ^ r%4 counted a
+// conflict in every second cycle).
 __device__ __forceinline__ int spread(int r) { return ((r >> 1) & 3) | (((r >> 4) & 1) << 2); }
 
 template <int FMT, bool COL, int B, int NW>
@@ -199,7 +201,7 @@ struct Operand {
   static constexpr int kRowB = B * 2;              // COL: bytes of a contraction row
   static constexpr int kLanes = COL ? (kRowB / 16) : 8;   // lanes on one row of a copy
   static constexpr int kRows = 64 / kLanes;        // rows of a copy
-  static constexpr int kSwz = B >= 128 ? 7 : B / 16 - 1;   // COL: a row's chunks are that many and one more, or twice
+  __device__ __forceinline__ static int chunk_swizzle(int r) { return B >= 128 ? 2 * (r & 3) : B == 64 ? r & 2 : 0; }
   static constexpr int kTiles = 4;                 // fragments a wave may hold
   static_assert(B / 8 % NW == 0 && kRowB <= 1024, "whole copies");
   // not COL: spread() of a copy's rows changes with 16 rows, so with the copy where fewer than 4 waves share them
@@ -224,10 +226,10 @@ struct Operand {
     if constexpr (COL) {
       rows = n;
       width = c_bytes;
-      const int g = ((row & 3) | (((row >> 3) & 1) << 2)) & kSwz;
+      const int g = chunk_swizzle(row);
       voff[0] = (uint32_t)(row * (int)ld + (((pos >> 1) ^ g) * 2 + (pos & 1)) * 16);
       // 16 lanes read values 16 (l/16%2).. of contraction rows 8 (l/32) + l%16/4
-      const int j = (lane & 15) >> 2, h = lane >> 5, gr = (j | (h << 2)) & kSwz;
+      const int j = (lane & 15) >> 2, h = lane >> 5, gr = chunk_swizzle(j);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
         rd[t] = (8 * h + j) * kRowB + (((w0 / 16 + 2 * t + ((lane >> 4) & 1)) ^ gr) * 32) + (lane & 3) * 8;
@@ -345,7 +347,8 @@ struct TileBody {
 
   // LDS stages of P and of Q: for 8 waves what fits in 160 KB (MX: with two of scales), for 4 two of each, so that two
   // workgroups share a CU
-  static constexpr int kPS = ONE ? 1 : NW == 4 ? 2 : MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4, kQS = ONE ? 1 : NW == 4 || BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
+  static constexpr int kPS = ONE ? 1 : NW == 4 ? 2 : MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4;
+  static constexpr int kQS = ONE ? 1 : NW == 4 || BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
   static constexpr int kPB = BI * kStageBytes, kQB = BJ * kStageBytes, kSB = MX ? (BI + BJ) * 16 : 0;
   static constexpr int kPC = OpP::kCopies, kQC = OpQ::kCopies;
   static constexpr int kTurn = NW * 32 * (BI / WI * 4 + 16);   // what store() needs for FP32
@@ -565,7 +568,8 @@ struct TileBody {
   // of 8 bytes the same stores cost 2.4 times as long (weight gradients of 48
   // experts, 2.8 GB: 885 us of the call).
   // Each wave turns 32 rows at a time in LDS of its own.
-  template <int TYPE>
+  // PAST: past the caches (see launch()).
+  template <int TYPE, bool PAST>
   __device__ __forceinline__ void store_as(const RaggedParams& p, int64_t base, int64_t row0, int i0, int ni, int nj) {
     constexpr int kW = BI / WI, kSize = TYPE == TYPE_F32 ? 4 : 2;   // columns of a wave
     constexpr int kRow = kW * kSize, kPitch = kRow + 16;            // 16 bytes more: rows on other banks
@@ -590,9 +594,12 @@ struct TileBody {
       for (int r = 0; r < 32; r += kRows) {
         const int j = r + lane / kLanes, jj = wj * (BJ / WJ) + 32 * u + j;
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(buf + j * kPitch + (lane % kLanes) * 16);
-        if (jj < nj && col < ni)
-          __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(static_cast<char*>(p.out) +
-                                                                   (base + (row0 + jj) * p.out_ld + i0 + col) * kSize));
+        if (jj < nj && col < ni) {
+          u32x4_t* at = reinterpret_cast<u32x4_t*>(static_cast<char*>(p.out) +
+                                                   (base + (row0 + jj) * p.out_ld + i0 + col) * kSize);
+          if constexpr (PAST) __builtin_nontemporal_store(w, at);
+          else *at = w;
+        }
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -600,9 +607,15 @@ struct TileBody {
 
   __device__ __forceinline__ void store(const RaggedParams& p, int64_t base, int64_t row0, int i0, int ni, int nj) {
     fence<0>();   // every wave is past its last fragments
-    if (p.out_type == TYPE_BF16) store_as<TYPE_BF16>(p, base, row0, i0, ni, nj);
-    else if (p.out_type == TYPE_F16) store_as<TYPE_F16>(p, base, row0, i0, ni, nj);
-    else store_as<TYPE_F32>(p, base, row0, i0, ni, nj);
+    if (p.stream_out) store_any<true>(p, base, row0, i0, ni, nj);
+    else store_any<false>(p, base, row0, i0, ni, nj);
+  }
+
+  template <bool PAST>
+  __device__ __forceinline__ void store_any(const RaggedParams& p, int64_t base, int64_t row0, int i0, int ni, int nj) {
+    if (p.out_type == TYPE_BF16) store_as<TYPE_BF16, PAST>(p, base, row0, i0, ni, nj);
+    else if (p.out_type == TYPE_F16) store_as<TYPE_F16, PAST>(p, base, row0, i0, ni, nj);
+    else store_as<TYPE_F32, PAST>(p, base, row0, i0, ni, nj);
   }
 
   __device__ __forceinline__ static void run(const RaggedParams& p, int e, const Group& g, int i0, int j0, int ni,
@@ -784,8 +797,7 @@ int64_t tile_bound(const RaggedParams& p, int B) {
 //   LARGE  256 x 256, 8 waves, a workgroup per CU: a step (64 values, 256 in FP4) 1.0 alone to 1.75 on all CUs, less
 //          where a group's last tile has fewer rows, 10 besides
 //   TWO    128 x 128, 4 waves, two a CU: 0.65 to 1.0 a step, 5 besides
-//   FOUR   the same in one LDS stage, four a CU that cover for each other: 0.95 to 2.0, 6 besides (14 where output
-//          rows do not begin on 128-byte lines: twice the writes)
+//   FOUR   the same in one LDS stage, four a CU that cover for each other: 0.95 to 2.0, 6 besides
 //   SPLIT  64 x 64, the contraction split over 4 waves: 0.75 for four steps, 4 besides
 // Measured in us (rows in all, N, K):       LARGE   TWO  FOUR SPLIT
 //   48 experts, 24576, 4096, 7168            1467          2327
@@ -813,11 +825,10 @@ Form form_of(const RaggedParams& p) {
   const double bytes = QC ? (double)p.M * (p.I + p.J) * 2 + (double)p.E * p.I * p.J * osize
                           : live * p.I * p.C * size + (double)p.M * (p.C * size + p.I * osize);
   const double n0 = tiles(256), n1 = tiles(128), n2 = tiles(64);
-  const bool lines = p.out_ld * (int64_t)osize % 128 == 0;
   const double us[4] = {
       __builtin_ceil(n0 / 256) * (steps * (1.0 + 0.75 * busy(n0, 256)) * part + 10),
       __builtin_ceil(n1 / 512) * (steps * (0.65 + 0.35 * busy(n1, 512)) * few + 5),
-      __builtin_ceil(n1 / 1024) * (steps * (0.95 + 1.05 * busy(n1, 1024)) * few + (lines ? 6 : 14)),
+      __builtin_ceil(n1 / 1024) * (steps * (0.95 + 1.05 * busy(n1, 1024)) * few + 6),
       __builtin_ceil(n2 / 256) * (__builtin_ceil(steps / 4) * 0.75 + 4)};
   int best = LARGE;
   double least = 0;
@@ -829,9 +840,17 @@ Form form_of(const RaggedParams& p) {
 }
 
 template <int FMT, bool PC, bool QC>
-hipError_t launch(const RaggedParams& p, hipStream_t s) {
+hipError_t launch(RaggedParams p, hipStream_t s) {
   if (!QC && p.M == 0) return hipSuccess;
   const Form f = form_of<FMT, QC>(p);
+  const int64_t size = p.out_type == TYPE_F32 ? 4 : 2;
+  const int64_t bytes = (QC ? (int64_t)p.E * p.J : p.M) * p.I * size;
+  // Whole lines that the L2s (32 MB) cannot hold leave them to the operands when they pass them by: FP4, 8 experts of
+  // 2048 rows 230 against 252 us. FOUR's calls are bound by such writes, and up to 256 MB the last-level cache takes
+  // them sooner: 21 against 27 us for 141 MB. Rows that begin inside a line need the caches to put lines together
+  // (24 against 70 us).
+  p.stream_out = p.out_ld * size % 128 == 0 && (uintptr_t)p.out % 128 == 0 &&
+                 bytes > ((int64_t)(f == FOUR ? 256 : 64) << 20);
   const int64_t grid = tile_bound<QC>(p, f == LARGE ? 256 : f == SPLIT ? 64 : 128);
   if (grid > 0x7FFFFFFF - kDealSlack) return hipErrorInvalidConfiguration;
   const unsigned n = (unsigned)grid + kDealSlack;
