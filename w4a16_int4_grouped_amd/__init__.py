@@ -497,23 +497,17 @@ def router_topk_grad(logits, ids, d_w, score="softmax", renorm=False, scale=1.0,
     _dense(d_w, "d_w", torch.float32, dev, (T, topk))
     if out is None:
         out = _new((T, E), logits.dtype, dev, stream)
-    o_ld = _matrix(out, "out", logits.dtype, dev, (T, E))
+        o_ld = E
+    else:
+        o_ld = _matrix(out, "out", logits.dtype, dev, (T, E))
     _call((_lib or lib()).moe_router_topk_grad, dev, stream,
           logits.data_ptr(), _dtype(logits.dtype), max(ld, E), T, E, topk, SCORES[score], 1 if renorm else 0, scale,
           ids.data_ptr(), d_w.data_ptr(), out.data_ptr(), max(o_ld, E))
     return out
 
 
-def _groups(offsets, device, E=None):
-    _need(offsets.dim() == 1 and offsets.shape[0] >= 2, "offsets: [E + 1]")
-    if E is None:
-        E = offsets.shape[0] - 1
-    _dense(offsets, "offsets", _torch.int32, device, (E + 1,))
-    return E
-
-
 def _weights(w, dtype, device):
-    _need(w.dim() == 3, "w: [E, N, K]")
+    """Row and expert distances of w [E, N, K]."""
     ld = _matrix(w, "w", dtype, device)
     return ld, (w.stride(0) if w.shape[0] > 1 else 0)
 
@@ -535,10 +529,12 @@ def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
     dev = a.device
     a_ld = _matrix(a, "a")
     w_ld, w_stride = _weights(w, a.dtype, dev)
-    _groups(offsets, dev, E)
+    _dense(offsets, "offsets", _torch.int32, dev, (E + 1,))
     if out is None:
         out = _new((M, N), out_dtype or a.dtype, dev, stream)
-    o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
+        o_ld = N
+    else:
+        o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
     _call((_lib or lib()).moe_grouped_gemm, dev, stream,
           a.data_ptr(), a_ld, w.data_ptr(), w_stride, w_ld, _dtype(a.dtype), offsets.data_ptr(), E, M, N, K,
           out.data_ptr(), o_ld, _dtype(out.dtype))
@@ -557,10 +553,12 @@ def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
     dev = dy.device
     y_ld = _matrix(dy, "dy")
     w_ld, w_stride = _weights(w, dy.dtype, dev)
-    _groups(offsets, dev, E)
+    _dense(offsets, "offsets", _torch.int32, dev, (E + 1,))
     if out is None:
         out = _new((M, K), out_dtype or dy.dtype, dev, stream)
-    o_ld = _matrix(out, "out", out_dtype, dev, (M, K))
+        o_ld = K
+    else:
+        o_ld = _matrix(out, "out", out_dtype, dev, (M, K))
     _call((_lib or lib()).moe_grouped_gemm_dgrad, dev, stream,
           dy.data_ptr(), y_ld, w.data_ptr(), w_stride, w_ld, _dtype(dy.dtype), offsets.data_ptr(), E, M, N, K,
           out.data_ptr(), o_ld, _dtype(out.dtype))
@@ -578,7 +576,9 @@ def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
     dev = dy.device
     y_ld = _matrix(dy, "dy")
     a_ld = _matrix(a, "a", dy.dtype, dev)
-    E = _groups(offsets, dev)
+    _need(offsets.dim() == 1 and offsets.shape[0] >= 2, "offsets: [E + 1]")
+    E = offsets.shape[0] - 1
+    _dense(offsets, "offsets", _torch.int32, dev, (E + 1,))
     if out is None:
         out = _new((E, N, K), out_dtype or dy.dtype, dev, stream)
     o_ld = _matrix(out, "out", out_dtype, dev, (E, N, K))
@@ -635,8 +635,10 @@ def mx_dequant(q, scales, dtype=None, out=None, stream=None):
     _dense(scales, "scales", torch.uint8, dev, lead + (mx_scale_cols(K),))
     if out is None:
         out = _new(lead + (K,), dtype or torch.bfloat16, dev, stream)
-    ld = _matrix(out, "out", dtype, dev, lead + (K,))
-    _need(out.dim() == 2 or out.is_contiguous(), "out: more than two dimensions must be contiguous")
+        ld = K
+    else:
+        ld = _matrix(out, "out", dtype, dev, lead + (K,))
+        _need(out.dim() == 2 or out.is_contiguous(), "out: more than two dimensions must be contiguous")
     _call((_lib or lib()).moe_mx_dequant, dev, stream,
           q.data_ptr(), scales.data_ptr(), q.numel() * 2 // K, K, out.data_ptr(), _dtype(out.dtype),
           ld if out.dim() == 2 else K)
@@ -656,10 +658,12 @@ def mx_grouped_gemm(aq, a_scales, wq, w_scales, offsets, out=None, out_dtype=Non
     _dense(a_scales, "a_scales", torch.uint8, dev, (M, cols))
     _dense(wq, "wq", torch.uint8, dev, (E, N, K // 2))
     _dense(w_scales, "w_scales", torch.uint8, dev, (E, N, cols))
-    _groups(offsets, dev, E)
+    _dense(offsets, "offsets", _torch.int32, dev, (E + 1,))
     if out is None:
         out = _new((M, N), out_dtype or torch.bfloat16, dev, stream)
-    o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
+        o_ld = N
+    else:
+        o_ld = _matrix(out, "out", out_dtype, dev, (M, N))
     _call((_lib or lib()).moe_mx_grouped_gemm, dev, stream,
           aq.data_ptr(), a_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), E, M, N, K,
           out.data_ptr(), o_ld, _dtype(out.dtype))
