@@ -476,7 +476,7 @@ def router_topk(logits, topk, score="softmax", bias=None, renorm=False, scale=1.
         _dense(ids, "ids", torch.int32, dev, (T, topk))
         _dense(w, "weights", torch.float32, dev, (T, topk))
     _call((_lib or lib()).moe_router_topk, dev, stream,
-          logits.data_ptr(), _dtype(logits.dtype), max(ld, E), T, E, topk, SCORES[score],
+          logits.data_ptr(), _dtype(logits.dtype), ld, T, E, topk, SCORES[score],
           None if bias is None else bias.data_ptr(), 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr())
     return ids, w
 
@@ -501,8 +501,8 @@ def router_topk_grad(logits, ids, d_w, score="softmax", renorm=False, scale=1.0,
     else:
         o_ld = _matrix(out, "out", logits.dtype, dev, (T, E))
     _call((_lib or lib()).moe_router_topk_grad, dev, stream,
-          logits.data_ptr(), _dtype(logits.dtype), max(ld, E), T, E, topk, SCORES[score], 1 if renorm else 0, scale,
-          ids.data_ptr(), d_w.data_ptr(), out.data_ptr(), max(o_ld, E))
+          logits.data_ptr(), _dtype(logits.dtype), ld, T, E, topk, SCORES[score], 1 if renorm else 0, scale,
+          ids.data_ptr(), d_w.data_ptr(), out.data_ptr(), o_ld)
     return out
 
 
