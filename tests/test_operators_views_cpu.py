@@ -75,3 +75,28 @@ def test_rows_closer_than_their_width(stride):
     refused(M.grouped_gemm_wgrad, view, Standin((6, 32), B), off)
     refused(M.mx_quant, view)
     refused(M.mx_dequant, Standin((6, 32), torch.uint8), Standin((6, 16), torch.uint8), out=view)
+
+
+BIG = (1 << 32) + 2     # 2 in 32 bits
+
+
+def test_sizes_past_32_bits():
+    ids, w = Standin((BIG, 1), I), Standin((BIG, 1), F)
+    refused(M.router_topk, Standin((BIG, 8), B), 1)
+    refused(M.router_topk, Standin((2, BIG), B), 1)
+    refused(M.router_topk, Standin((2, 8), B), BIG)
+    refused(M.router_topk_grad, Standin((BIG, 8), B), ids, w)
+    refused(M.router_topk_grad, Standin((2, BIG), B), Standin((2, 1), I), Standin((2, 1), F))
+    off, wide = Standin((3,), I), (1 << 32) + 64
+    refused(M.grouped_gemm, Standin((BIG, 64), B), Standin((2, 32, 64), B), off)
+    refused(M.grouped_gemm, Standin((2, wide), B, (64, 1)), Standin((2, 32, wide), B, (2048, 64, 1)), off)
+    refused(M.grouped_gemm, Standin((2, 64), B), Standin((2, wide, 64), B), off, out=Standin((2, wide), B, (64, 1)))
+    refused(M.grouped_gemm_dgrad, Standin((BIG, 64), B), Standin((2, 64, 32), B), off)
+    refused(M.grouped_gemm_wgrad, Standin((BIG, 64), B), Standin((BIG, 32), B), off)
+    refused(M.mx_scale_cols, (1 << 32) + 32)
+    refused(M.mx_quant, Standin((2, (1 << 32) + 32), B, (32, 1)))
+    u8 = torch.uint8
+    refused(M.mx_grouped_gemm, Standin((BIG, 32), u8), Standin((BIG, 16), u8), Standin((2, 8, 32), u8),
+            Standin((2, 8, 16), u8), off)
+    refused(M.mx_grouped_gemm, Standin((2, 32), u8), Standin((2, 16), u8), Standin((2, BIG + 6, 32), u8),
+            Standin((2, BIG + 6, 16), u8), off)

@@ -402,6 +402,12 @@ def _need(ok, msg):
         raise MoeError(MOE_ERR_INVALID_ARG, msg)
 
 
+def _fits(sizes):
+    """Refuses sizes (joined by |) past 31 bits, which the library's arguments would cut off."""
+    if sizes >> 31:
+        raise MoeError(MOE_ERR_INVALID_ARG, "a size of 2^31 or more")
+
+
 def _matrix(t, name, dtype=None, device=None, shape=None):
     """Checks a tensor's rows: on the GPU (the first operand's), of a dtype
     and shape, values of a row adjacent. Returns the row distance."""
@@ -466,6 +472,7 @@ def router_topk(logits, topk, score="softmax", bias=None, renorm=False, scale=1.
     if score not in SCORES:
         raise MoeError(MOE_ERR_INVALID_ARG, f"score {score!r}: softmax or sigmoid")
     _need(topk >= 1, "topk: at least 1")
+    _fits(T | E | topk)
     if bias is not None:
         _dense(bias, "bias", torch.float32, dev, (E,))
     if out is None:
@@ -491,6 +498,7 @@ def router_topk_grad(logits, ids, d_w, score="softmax", renorm=False, scale=1.0,
     ld = _matrix(logits, "logits")
     dev = logits.device
     topk = ids.shape[1]
+    _fits(T | E | topk)
     if score not in SCORES:
         raise MoeError(MOE_ERR_INVALID_ARG, f"score {score!r}: softmax or sigmoid")
     _dense(ids, "ids", torch.int32, dev, (T, topk))
@@ -526,6 +534,7 @@ def grouped_gemm(a, w, offsets, out=None, out_dtype=None, stream=None):
     E, N, Kw = w.shape
     if K != Kw:
         raise MoeError(MOE_ERR_INVALID_ARG, f"a has {K} columns, w {Kw}")
+    _fits(M | N | K | E)
     dev = a.device
     a_ld = _matrix(a, "a")
     w_ld, w_stride = _weights(w, a.dtype, dev)
@@ -550,6 +559,7 @@ def grouped_gemm_dgrad(dy, w, offsets, out=None, out_dtype=None, stream=None):
     E, Nw, K = w.shape
     if N != Nw:
         raise MoeError(MOE_ERR_INVALID_ARG, f"dy has {N} columns, w {Nw} rows")
+    _fits(M | N | K | E)
     dev = dy.device
     y_ld = _matrix(dy, "dy")
     w_ld, w_stride = _weights(w, dy.dtype, dev)
@@ -578,6 +588,7 @@ def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
     a_ld = _matrix(a, "a", dy.dtype, dev)
     _need(offsets.dim() == 1 and offsets.shape[0] >= 2, "offsets: [E + 1]")
     E = offsets.shape[0] - 1
+    _fits(M | N | K | E)
     _dense(offsets, "offsets", _torch.int32, dev, (E + 1,))
     if out is None:
         out = _new((E, N, K), out_dtype or dy.dtype, dev, stream)
@@ -592,6 +603,7 @@ def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
 @functools.lru_cache(maxsize=None)
 def mx_scale_cols(K) -> int:
     """Bytes of a row of MXFP4 scales: K / 32 rounded up to a multiple of 16."""
+    _fits(K)
     n = lib().moe_mx_scale_cols(K)
     if n == 0:
         check(MOE_ERR_INVALID_ARG)
@@ -654,6 +666,7 @@ def mx_grouped_gemm(aq, a_scales, wq, w_scales, offsets, out=None, out_dtype=Non
     M, E, N, K = aq.shape[0], wq.shape[0], wq.shape[1], 2 * aq.shape[1]
     dev = aq.device
     cols = mx_scale_cols(K)
+    _fits(M | N | E)
     _dense(aq, "aq", torch.uint8, dev, (M, K // 2))
     _dense(a_scales, "a_scales", torch.uint8, dev, (M, cols))
     _dense(wq, "wq", torch.uint8, dev, (E, N, K // 2))
