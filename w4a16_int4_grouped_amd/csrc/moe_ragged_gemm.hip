@@ -67,9 +67,9 @@ __device__ __forceinline__ Group group_of(const RaggedParams& p, int e) {
 // operands, and one XCD's L2) dealt round-robin to the XCDs, so that each gets
 // its part of large and small experts; -1 past the last. A run is 16 items (8,
 // 32 and 64 measured within 3 %), less where that would leave XCDs without
-// one. The grid needs total + 8 * 16 workgroups.
-__device__ __forceinline__ int deal(int b, int total) {
-  const int G = min(max(total / 64, 1), 16);
+// one, but `least`. The grid needs total + 8 * 16 workgroups.
+__device__ __forceinline__ int deal(int b, int total, int least) {
+  const int G = min(max(total / 64, least), 16);
   const int idx = b >> 3, run = (idx / G) * 8 + (b & 7);
   const int t = run * G + idx % G;
   return t < total ? t : -1;
@@ -99,14 +99,20 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive
 }
 
 // The tile of workgroup b among all experts' tiles of BJ rows x NI columns,
-// experts in order. e < 0: none left. A lane adds up the tiles of ceil(E / 64)
-// neighbouring experts, a scan finds the lane that holds the tile, and with an
-// expert of that lane's per lane a second scan the expert: three loads one
-// after the other, whatever E.
-__device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, int NI) {
+// experts in order, and its expert's rows. e < 0: none left. A lane adds up the
+// tiles of ceil(E / 64) neighbouring experts, a scan finds the lane that holds
+// the tile, and with an expert of that lane's per lane a second scan the
+// expert: one load after another only for more than 64 experts, whatever E.
+struct Found {
+  Tile t;
+  Group g;
+};
+__device__ __forceinline__ Found find_tile(const RaggedParams& p, int b, int BJ, int NI, int least) {
   const int lane = threadIdx.x & 63, each = (p.E + 63) / 64;
   const int32_t* off = p.offsets;
+  const Found none = {{-1, 0, 0}, {0, 0}};
   int mine = 0;
+  Group g = {0, 0};
   {
     int e = lane * each;
     const int end = min(e + each, p.E);
@@ -114,38 +120,42 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, int b, int BJ, 
 #pragma unroll 8
     for (; e < end; ++e) {
       const int hi = off[e + 1];
-      const int from = min(max(lo, 0), p.M);
-      mine += (min(max(hi, from), p.M) - from + BJ - 1) / BJ;
+      g.lo = min(max(lo, 0), p.M);
+      g.n = min(max(hi, g.lo), p.M) - g.lo;
+      mine += (g.n + BJ - 1) / BJ;
       lo = hi;
     }
   }
   int sum = wave_scan(mine);
-  const int t = deal(b, __builtin_amdgcn_readlane(sum, 63) * NI);
-  if (t < 0) return Tile{-1, 0, 0};
+  const int t = deal(b, __builtin_amdgcn_readlane(sum, 63) * NI, least);
+  if (t < 0) return none;
   uint64_t past = __ballot(sum * NI > t);
-  if (!past) return Tile{-1, 0, 0};
-  int at = __builtin_ctzll(past);
-  const int before = __builtin_amdgcn_readlane(sum - mine, at), e0 = at * each;
-  const int e = e0 + lane;
-  const int n = lane < each && e < p.E ? (group_of(p, e).n + BJ - 1) / BJ : 0;
-  sum = wave_scan(n);
-  past = __ballot((before + sum) * NI > t);
-  if (!past) return Tile{-1, 0, 0};
-  at = __builtin_ctzll(past);
-  const int ne = __builtin_amdgcn_readlane(n, at);
-  const int local = t - (before + __builtin_amdgcn_readlane(sum, at) - ne) * NI;
-  const Tile tl = tile_of(e0 + at, local, ne, NI);
-  return Tile{__builtin_amdgcn_readfirstlane(tl.e), __builtin_amdgcn_readfirstlane(tl.it),
-              __builtin_amdgcn_readfirstlane(tl.jt)};
+  if (!past) return none;
+  int at = __builtin_ctzll(past), e0 = 0, before = 0;
+  if (each > 1) {
+    before = __builtin_amdgcn_readlane(sum - mine, at), e0 = at * each;
+    g = lane < each && e0 + lane < p.E ? group_of(p, e0 + lane) : Group{0, 0};
+    mine = (g.n + BJ - 1) / BJ;
+    sum = wave_scan(mine);
+    past = __ballot((before + sum) * NI > t);
+    if (!past) return none;
+    at = __builtin_ctzll(past);
+  }
+  const int nj = __builtin_amdgcn_readlane(mine, at);
+  const int local = t - (before + __builtin_amdgcn_readlane(sum, at) - nj) * NI;
+  const Tile tl = tile_of(e0 + at, local, nj, NI);
+  return Found{{__builtin_amdgcn_readfirstlane(tl.e), __builtin_amdgcn_readfirstlane(tl.it),
+                __builtin_amdgcn_readfirstlane(tl.jt)},
+               {__builtin_amdgcn_readlane(g.lo, at), __builtin_amdgcn_readlane(g.n, at)}};
 }
 
 // The same where every expert has J output rows (wgrad), tiles of BJ x BI.
-__device__ __forceinline__ Tile even_tile(const RaggedParams& p, int b, int BJ, int BI) {
+__device__ __forceinline__ Found even_tile(const RaggedParams& p, int b, int BJ, int BI, int least) {
   const int nj = (p.J + BJ - 1) / BJ, NI = (p.I + BI - 1) / BI;
-  const int t = deal(b, p.E * nj * NI);
-  if (t < 0) return Tile{-1, 0, 0};
+  const int t = deal(b, p.E * nj * NI, least);
+  if (t < 0) return Found{{-1, 0, 0}, {0, 0}};
   const int e = t / (nj * NI);
-  return tile_of(e, t - e * nj * NI, nj, NI);
+  return Found{tile_of(e, t - e * nj * NI, nj, NI), group_of(p, e)};
 }
 
 // Buffer descriptor of `bytes` bytes from p: loads past the last read 0.
@@ -641,10 +651,11 @@ __attribute__((amdgpu_waves_per_eu(ONE ? 4 : 2, ONE ? 4 : 2))) void ragged_gemm(
   using B1 = TileBody<FMT, PC, QC, BI, BJ / 4, kLarge ? WI : WI * 2, kLarge ? WJ : WJ / 2, ONE>;
   constexpr auto most = [](int a, int b) { return a > b ? a : b; };
   __shared__ __align__(1024) char lds[most(most(B4::kLds, B3::kLds), most(B2::kLds, B1::kLds))];
-  const Tile t = QC ? even_tile(p, blockIdx.x, BJ, BI) : find_tile(p, blockIdx.x, BJ, (p.I + BI - 1) / BI);
+  const Found f = QC ? even_tile(p, blockIdx.x, BJ, BI, 1) : find_tile(p, blockIdx.x, BJ, (p.I + BI - 1) / BI, 1);
+  const Tile t = f.t;
+  const Group g = f.g;
   if (t.e < 0) return;
   const int e = t.e;
-  const Group g = group_of(p, e);
   const int i0 = t.it * BI, j0 = t.jt * BJ;
   const int ni = min(p.I - i0, BI), nj = min((QC ? p.J : g.n) - j0, BJ);
   if (i0 < 0 || j0 < 0 || ni <= 0 || nj <= 0) return;   // sums of offsets that decrease may wrap
@@ -655,13 +666,17 @@ __attribute__((amdgpu_waves_per_eu(ONE ? 4 : 2, ONE ? 4 : 2))) void ragged_gemm(
   else B1::run(p, e, g, i0, j0, ni, nj, lds);
 }
 
-// One 64 x BJ tile of four waves that share its contraction: wave w takes steps
-// w, w + 4, .. on stages of its own, without a barrier, and the four FP32 sums
-// are added in wave order through LDS. For calls of few tiles, where a tile's
-// chain of steps is the time.
-template <int FMT, bool PC, bool QC, int BJ>
+// One BI x BJ tile of W waves that share its contraction: wave w takes steps w,
+// w + W, .. on stages of its own, without a barrier, and the W FP32 sums are
+// added in wave order through LDS. For calls of few tiles, where a tile's chain
+// of steps is the time: BI = 64 with 4 waves, or 32 with 6 (FP4 5), which LDS
+// has room for.
+template <int FMT, int BI>
+constexpr int kSplitWaves = BI == 64 ? 4 : FMT == FMT_MX ? 5 : 6;
+
+template <int FMT, bool PC, bool QC, int BI, int BJ>
 struct SplitBody {
-  static constexpr int BI = 64, W = 4, TI = 2, TJ = BJ / 32;
+  static constexpr int W = kSplitWaves<FMT, BI>, TI = BI / 32, TJ = BJ / 32;
   static constexpr bool MX = FMT == FMT_MX;
   static constexpr int kVal = MX ? 256 : 64;
   using OpP = Operand<FMT, PC, BI, 1>;
@@ -757,10 +772,8 @@ struct SplitBody {
         }
     __syncthreads();
     const int64_t at = QC ? (int64_t)e * p.out_stride + (int64_t)j0 * p.out_ld : (int64_t)(g.lo + j0) * p.out_ld;
-    const int i = (lane & 15) * 4;
-#pragma unroll
-    for (int r = 0; r < BJ / W; r += 4) {
-      const int j = wave * (BJ / W) + r + (lane >> 4);
+    const int i = (int)threadIdx.x % (BI / 4) * 4;
+    for (int j = (int)threadIdx.x / (BI / 4); j < BJ; j += 64 * W / (BI / 4)) {
       f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < W; ++w) v += *reinterpret_cast<const f32x4_t*>(all + w * (kLds / W) + j * kPitch + i * 4);
@@ -769,25 +782,29 @@ struct SplitBody {
   }
 };
 
-template <int FMT, bool PC, bool QC>
-__global__ __launch_bounds__(256) void ragged_split(RaggedParams p) {
-  using Wide = SplitBody<FMT, PC, QC, 64>;
-  using Narrow = SplitBody<FMT, PC, QC, 32>;
+template <int FMT, bool PC, bool QC, int BI>
+__global__ __launch_bounds__((64 * kSplitWaves<FMT, BI>)) void ragged_split(RaggedParams p) {
+  using Wide = SplitBody<FMT, PC, QC, BI, 64>;
+  using Narrow = SplitBody<FMT, PC, QC, BI, 32>;
   __shared__ __align__(1024) char lds[Wide::kLds > Narrow::kLds ? Wide::kLds : Narrow::kLds];
-  const Tile t = QC ? even_tile(p, blockIdx.x, 64, 64) : find_tile(p, blockIdx.x, 64, (p.I + 63) / 64);
+  // two tiles that read the halves of the same lines on one XCD (1 expert, 64 rows, 7168 by 1024: 14.7 against 25.7 us)
+  constexpr int kLeast = PC && BI == 32 ? 2 : 1;
+  const Found f = QC ? even_tile(p, blockIdx.x, 64, BI, kLeast)
+                     : find_tile(p, blockIdx.x, 64, (p.I + BI - 1) / BI, kLeast);
+  const Tile t = f.t;
+  const Group g = f.g;
   if (t.e < 0) return;
-  const Group g = group_of(p, t.e);
-  const int i0 = t.it * 64, j0 = t.jt * 64;
-  const int ni = min(p.I - i0, 64), nj = min((QC ? p.J : g.n) - j0, 64);
+  const int i0 = t.it * BI, j0 = t.jt * 64;
+  const int ni = min(p.I - i0, BI), nj = min((QC ? p.J : g.n) - j0, 64);
   if (i0 < 0 || j0 < 0 || ni <= 0 || nj <= 0) return;   // as above
   if (nj > 32) Wide::run(p, t.e, g, i0, j0, ni, nj, lds);
   else Narrow::run(p, t.e, g, i0, j0, ni, nj, lds);
 }
 
-// Tiles of B x B: at most, where groups are ragged.
+// Tiles of BI x B: at most, where groups are ragged.
 template <bool QC>
-int64_t tile_bound(const RaggedParams& p, int B) {
-  const int64_t NI = (p.I + B - 1) / B, live = p.E < p.M ? p.E : p.M;   // experts that can hold rows
+int64_t tile_bound(const RaggedParams& p, int BI, int B) {
+  const int64_t NI = (p.I + BI - 1) / BI, live = p.E < p.M ? p.E : p.M;   // experts that can hold rows
   return QC ? p.E * NI * ((p.J + B - 1) / B) : NI * ((p.M + live * (B - 1)) / B);
 }
 
@@ -799,14 +816,17 @@ int64_t tile_bound(const RaggedParams& p, int B) {
 //   TWO    128 x 128, 4 waves, two a CU: 0.65 to 1.0 a step, 5 besides
 //   FOUR   the same in one LDS stage, four a CU that cover for each other: 0.95 to 2.0, 6 besides
 //   SPLIT  64 x 64, the contraction split over 4 waves: 0.75 for four steps, 4 besides
-// Measured in us (rows in all, N, K):       LARGE   TWO  FOUR SPLIT
+//   THIN   32 x 64 over 6 waves (FP4: 5): 0.75 for six steps (0.5 on few CUs), 4 besides
+// Measured in us (rows in all, N, K):       LARGE   TWO  FOUR SPLIT  THIN
 //   48 experts, 24576, 4096, 7168            1467          2327
 //   384 experts, 32768, 7168, 256             517   514   409  2070
 //   16 experts, 8192, 2048, 1024               52    47    48   107
 //   1 expert, 1024, 4096, 4096                 74    47    68    59
-//   1 expert, 512, 512, 7168                  113    76   110    25
+//   1 expert, 250, 4872, 7168                               46    55
+//   1 expert, 512, 512, 7168                  113    76   110    25    20
+//   1 expert, 64, 1024, 7168                                20    14
 //   wgrad, 64 experts, 4000, 2048, 2048       134   130   107   717
-enum Form : int { LARGE = 0, TWO = 1, FOUR = 2, SPLIT = 3 };
+enum Form : int { LARGE = 0, TWO = 1, FOUR = 2, SPLIT = 3, THIN = 4 };
 
 template <int FMT, bool QC>
 Form form_of(const RaggedParams& p) {
@@ -814,9 +834,9 @@ Form form_of(const RaggedParams& p) {
   const double live = p.E < p.M ? p.E : p.M, rows = p.M / live;
   const double C = QC ? rows : p.C;
   const double steps = __builtin_ceil(C / (FMT == FMT_MX ? 256 : 64));
-  auto tiles = [&](int B) {
+  auto tiles = [&](int B, int BI) {
     return (QC ? p.E * __builtin_ceil((double)p.J / B) : live * __builtin_ceil(rows / B)) *
-           __builtin_ceil((double)p.I / B);
+           __builtin_ceil((double)p.I / BI);
   };
   auto busy = [](double n, double full) { return n < full ? n / full : 1.0; };
   const double j = QC ? p.J : rows;   // rows of an expert's tiles
@@ -824,15 +844,16 @@ Form form_of(const RaggedParams& p) {
   const double size = FMT == FMT_MX ? 17.0 / 32 : 2, osize = p.out_type == TYPE_F32 ? 4 : 2;
   const double bytes = QC ? (double)p.M * (p.I + p.J) * 2 + (double)p.E * p.I * p.J * osize
                           : live * p.I * p.C * size + (double)p.M * (p.C * size + p.I * osize);
-  const double n0 = tiles(256), n1 = tiles(128), n2 = tiles(64);
-  const double us[4] = {
+  const double n0 = tiles(256, 256), n1 = tiles(128, 128), n2 = tiles(64, 64), n3 = tiles(64, 32);
+  const double us[5] = {
       __builtin_ceil(n0 / 256) * (steps * (1.0 + 0.75 * busy(n0, 256)) * part + 10),
       __builtin_ceil(n1 / 512) * (steps * (0.65 + 0.35 * busy(n1, 512)) * few + 5),
       __builtin_ceil(n1 / 1024) * (steps * (0.95 + 1.05 * busy(n1, 1024)) * few + 6),
-      __builtin_ceil(n2 / 256) * (__builtin_ceil(steps / 4) * 0.75 + 4)};
+      __builtin_ceil(n2 / 256) * (__builtin_ceil(steps / 4) * 0.75 + 4),
+      __builtin_ceil(n3 / 256) * (__builtin_ceil(steps / kSplitWaves<FMT, 32>) * 0.75 + 4)};
   int best = LARGE;
   double least = 0;
-  for (int f = LARGE; f <= SPLIT; ++f) {
+  for (int f = LARGE; f <= THIN; ++f) {
     const double t = us[f] > bytes / 5.5e6 ? us[f] : bytes / 5.5e6;
     if (f == LARGE || t < least) best = f, least = t;
   }
@@ -851,13 +872,15 @@ hipError_t launch(RaggedParams p, hipStream_t s) {
   // (24 against 70 us).
   p.stream_out = p.out_ld * size % 128 == 0 && (uintptr_t)p.out % 128 == 0 &&
                  bytes > ((int64_t)(f == FOUR ? 256 : 64) << 20);
-  const int64_t grid = tile_bound<QC>(p, f == LARGE ? 256 : f == SPLIT ? 64 : 128);
+  const int64_t grid = tile_bound<QC>(p, f == LARGE ? 256 : f == SPLIT ? 64 : f == THIN ? 32 : 128,
+                                      f == LARGE ? 256 : f >= SPLIT ? 64 : 128);
   if (grid > 0x7FFFFFFF - kDealSlack) return hipErrorInvalidConfiguration;
   const unsigned n = (unsigned)grid + kDealSlack;
   if (f == LARGE) ragged_gemm<FMT, PC, QC, 256, 256, 4, 2, false><<<n, 512, 0, s>>>(p);
   else if (f == TWO) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, false><<<n, 256, 0, s>>>(p);
   else if (f == FOUR) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, true><<<n, 256, 0, s>>>(p);
-  else ragged_split<FMT, PC, QC><<<n, 256, 0, s>>>(p);
+  else if (f == SPLIT) ragged_split<FMT, PC, QC, 64><<<n, 64 * kSplitWaves<FMT, 64>, 0, s>>>(p);
+  else ragged_split<FMT, PC, QC, 32><<<n, 64 * kSplitWaves<FMT, 32>, 0, s>>>(p);
   return hipGetLastError();
 }
 
