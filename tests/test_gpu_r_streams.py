@@ -1,0 +1,52 @@
+"""Calls on a stream other than the current one: what they allocate comes from
+that stream's memory, and their results are those of the current stream."""
+import pytest
+import torch
+
+from tests.gpu_util import log, require_gpu
+from tests.ops_util import offsets_of
+
+pytestmark = pytest.mark.gpu
+
+
+def operator_calls(M):
+    """name -> call(stream) with outputs of 2 MB and more."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    T, N, K = 4096, 512, 512
+    x, dy, w, off = r(T, K).bfloat16(), r(T, N).bfloat16(), r(2, N, K).bfloat16(), offsets_of([T - 5, 5]).cuda()
+    logits, d_w = r(T, 256), r(T, 64)
+    ids, _ = M.router_topk(logits, 64)
+    q, wq = M.mx_quant(x), M.mx_quant(w)
+    return {
+        "router_topk": lambda s: M.router_topk(logits, 64, stream=s),
+        "router_topk_grad": lambda s: M.router_topk_grad(logits, ids, d_w, stream=s),
+        "grouped_gemm": lambda s: M.grouped_gemm(x, w, off, stream=s),
+        "grouped_gemm_dgrad": lambda s: M.grouped_gemm_dgrad(dy, w, off, stream=s),
+        "grouped_gemm_wgrad": lambda s: M.grouped_gemm_wgrad(dy, x, off, out_dtype=torch.float32, stream=s),
+        "mx_quant": lambda s: M.mx_quant(x, stream=s),
+        "mx_dequant": lambda s: M.mx_dequant(*q, stream=s),
+        "mx_grouped_gemm": lambda s: M.mx_grouped_gemm(*q, *wq, off, stream=s),
+    }
+
+
+def tensors(out):
+    return out if isinstance(out, tuple) else (out,)
+
+
+def test_operators_do_not_reuse_the_current_streams_memory():
+    require_gpu()
+    import w4a16_int4_grouped_amd as M
+    side = torch.cuda.Stream()
+    for name, call in operator_calls(M).items():
+        log(f"case stream memory {name}")
+        want = tensors(call(None))
+        torch.cuda.synchronize()
+        free = [torch.empty_like(t) for t in want]            # blocks of the same sizes, given back to this stream
+        places = {t.data_ptr() for t in free}
+        del free
+        got = tensors(call(side))
+        side.synchronize()
+        assert not places & {t.data_ptr() for t in got}, name
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), name

@@ -438,11 +438,18 @@ def _dense(t, name, dtype, device, shape):
 
 
 def _new(shape, dtype, device, stream):
-    """An output; on a stream other than the current one, kept from reuse until that stream is done with it."""
-    t = _torch.empty(*shape, dtype=dtype, device=device)   # a tuple is read 0.1 us slower
+    """An output. For a stream other than the current one it is made on that
+    stream, because memory freed on the current one may still be in use by what
+    is queued there, and it is kept from reuse until both are done with it."""
+    torch = _torch
     if stream is not None:
-        t.record_stream(stream)
-    return t
+        current = torch.cuda.current_stream(device)
+        if stream.cuda_stream != current.cuda_stream:
+            with torch.cuda.stream(stream):
+                t = torch.empty(*shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    return torch.empty(*shape, dtype=dtype, device=device)   # a tuple is read 0.1 us slower
 
 
 def _call(fn, device, stream, *args):
