@@ -50,3 +50,29 @@ def test_operators_do_not_reuse_the_current_streams_memory():
         assert not places & {t.data_ptr() for t in got}, name
         for a, b in zip(got, want):
             assert torch.equal(a, b), name
+
+
+def test_the_layer_does_not_reuse_the_current_streams_memory():
+    """Its output, and the workspace that it gives back on return: calls queued on two streams, bit for bit the calls
+    made one at a time."""
+    require_gpu()
+    import w4a16_int4_grouped_amd as M
+    from tests.test_gpu_n_operators import tiny_handle
+    E, H, I, T, topk = 16, 1024, 512, 2000, 4
+    log("case stream memory of the layer")
+    h = tiny_handle(E, H, I)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    routes = [M.router_topk(torch.randn(T, E, generator=g, device="cuda"), topk, renorm=True) for _ in range(2)]
+    want = [h.indexed(x, *r) for r in routes]
+    nbytes = h.workspace_bytes(T, topk, T)
+    torch.cuda.synchronize()
+    free = [torch.empty_like(want[0]), torch.empty(nbytes, dtype=torch.uint8, device="cuda")]
+    places = {t.data_ptr() for t in free}
+    del free
+    side = torch.cuda.Stream()
+    got = [(h.indexed(x, *routes[k % 2], stream=side), h.indexed(x, *routes[1 - k % 2])) for k in range(4)]
+    torch.cuda.synchronize()
+    assert not places & {o.data_ptr() for o, _ in got}
+    for k, (a, b) in enumerate(got):
+        assert torch.equal(a, want[k % 2]) and torch.equal(b, want[1 - k % 2]), k

@@ -161,13 +161,24 @@ def check(status: int) -> None:
 # torch plumbing (device memory and streams only)
 # ---------------------------------------------------------------------------
 
+_torch = None
+_CODES = None       # torch dtype -> MOE_DTYPE_*
+
+
+def _load():
+    global _torch, _CODES
+    import torch
+    _CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
+    _torch = torch
+    return torch
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
 def _stream(stream=None):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
+    s = stream if stream is not None else (_torch or _load()).cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
 
@@ -180,9 +191,24 @@ def _tuning(ovr):
                                int(ovr.get("dispatch", 0)), int(ovr.get("global_experts", 0))))
 
 
-def _empty(nbytes, device):
-    import torch
-    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+def _new(shape, dtype, device, stream):
+    """A buffer of a call. For a stream other than the current one it is made
+    on that stream, because memory freed on the current one may still be in use
+    by what is queued there, and kept from reuse until both are done with it."""
+    torch = _torch or _load()
+    if stream is not None:
+        current = torch.cuda.current_stream(device)
+        if stream.cuda_stream != current.cuda_stream:
+            with torch.cuda.stream(stream):
+                t = torch.empty(*shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    return torch.empty(*shape, dtype=dtype, device=device)   # a tuple is read 0.1 us slower
+
+
+def _empty(nbytes, device, stream):
+    """A workspace."""
+    return _new((max(int(nbytes), 1),), (_torch or _load()).uint8, device, stream)
 
 
 class PreparedWeights:
@@ -205,7 +231,7 @@ class PreparedWeights:
         nbytes = L.moe_prepared_bytes(ctypes.byref(desc))
         if nbytes == 0:
             raise MoeError(MOE_ERR_UNSUPPORTED_SCHEMA, last_error())
-        self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self.buffer = _new((nbytes,), torch.uint8, self.device, stream)
         h = ctypes.c_void_p()
         check(L.moe_prepare_weights(ctypes.byref(desc), _ptr(w13_q), _ptr(w13_s), _ptr(w2_q), _ptr(w2_s),
                                     _ptr(self.buffer), nbytes, _stream(stream), ctypes.byref(h)))
@@ -230,7 +256,7 @@ class PreparedWeights:
         if nbytes == 0:
             check(MOE_ERR_INVALID_ARG)
         if routing is None:
-            routing = torch.empty(nbytes // 4, dtype=torch.int32, device=self.device)
+            routing = _new((nbytes // 4,), torch.int32, self.device, stream)
         check(lib().moe_align(self.handle, _ptr(topk_ids), T, topk, _tuning(ovr), _ptr(routing),
                               routing.numel() * routing.element_size(), _stream(stream)))
         return routing
@@ -244,7 +270,7 @@ class PreparedWeights:
         if nbytes == 0:
             check(MOE_ERR_INVALID_ARG)
         if routing is None:
-            routing = torch.empty(nbytes // 4, dtype=torch.int32, device=self.device)
+            routing = _new((nbytes // 4,), torch.int32, self.device, stream)
         check(lib().moe_align_ep(self.handle, _ptr(topk_ids), T, topk, _ptr(expert_map), num_global_experts,
                                  _tuning(ovr), _ptr(routing), routing.numel() * routing.element_size(),
                                  _stream(stream)))
@@ -257,9 +283,9 @@ class PreparedWeights:
         T = x.shape[0]
         L = self.routing_layout(T, topk, ovr)
         if out is None:
-            a = torch.empty((L.cap, self.H), dtype=torch.bfloat16, device=self.device)
-            m = torch.empty(L.cap, dtype=torch.int32, device=self.device)
-            r = torch.empty(L.cap, dtype=torch.int32, device=self.device)
+            a = _new((L.cap, self.H), torch.bfloat16, self.device, stream)
+            m = _new((L.cap,), torch.int32, self.device, stream)
+            r = _new((L.cap,), torch.int32, self.device, stream)
         else:
             a, m, r = out
             if (a.dtype != torch.bfloat16 or m.dtype != torch.int32 or r.dtype != torch.int32
@@ -280,9 +306,9 @@ class PreparedWeights:
         import torch
         T, topk = topk_ids.shape
         if out is None:
-            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            out = _new((T, self.H), torch.bfloat16, self.device, stream)
         if ws is None:
-            ws = _empty(self.workspace_bytes(T, topk, T, ovr=ovr), self.device)
+            ws = _empty(self.workspace_bytes(T, topk, T, ovr=ovr), self.device, stream)
         check(lib().moe_w4a16_indexed(self.handle, _ptr(x), T, topk, _ptr(topk_ids), _ptr(topk_w),
                                       _ptr(routing), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
                                       _tuning(ovr), _stream(stream)))
@@ -302,9 +328,9 @@ class PreparedWeights:
         M_pad = a.shape[0]
         if out is None:
             rows = T if row_src is not None else M_pad
-            out = torch.empty((rows, self.H), dtype=torch.bfloat16, device=self.device)
+            out = _new((rows, self.H), torch.bfloat16, self.device, stream)
         if ws is None:
-            ws = _empty(self.workspace_bytes(M_pad, topk if row_src is not None else 0, T), self.device)
+            ws = _empty(self.workspace_bytes(M_pad, topk if row_src is not None else 0, T), self.device, stream)
         check(lib().moe_w4a16_contiguous(self.handle, _ptr(a), M_pad, _ptr(m_indices), _ptr(row_src),
                                          _ptr(topk_w), T, topk, _ptr(out), _ptr(ws),
                                          ws.numel() * ws.element_size(), _tuning(ovr), _stream(stream)))
@@ -314,9 +340,9 @@ class PreparedWeights:
         import torch
         E, max_m, H = a3.shape
         if out is None:
-            out = torch.empty((E * max_m, self.H), dtype=torch.bfloat16, device=self.device)
+            out = _new((E * max_m, self.H), torch.bfloat16, self.device, stream)
         if ws is None:
-            ws = _empty(self.workspace_bytes(max_m), self.device)
+            ws = _empty(self.workspace_bytes(max_m), self.device, stream)
         check(lib().moe_w4a16_masked(self.handle, _ptr(a3), max_m, _ptr(masked_m), expected_m, _ptr(out),
                                      _ptr(ws), ws.numel() * ws.element_size(), _tuning(ovr), _stream(stream)))
         return out
@@ -328,7 +354,7 @@ class PreparedWeights:
         T = x.shape[0]
         if out is None:
             cap = self.routing_layout(T, topk, ovr).cap
-            out = torch.empty((cap, 2 * self.I), dtype=torch.bfloat16, device=self.device)
+            out = _new((cap, 2 * self.I), torch.bfloat16, self.device, stream)
         check(lib().moe_w4a16_gate_up(self.handle, _ptr(x), T, topk, _ptr(routing), _ptr(out), _tuning(ovr),
                                       _stream(stream)))
         return out
@@ -337,7 +363,7 @@ class PreparedWeights:
         """BF16 [cap, H] rows of the second GEMM at the routing's slots."""
         import torch
         if out is None:
-            out = torch.empty((a.shape[0], self.H), dtype=torch.bfloat16, device=self.device)
+            out = _new((a.shape[0], self.H), torch.bfloat16, self.device, stream)
         check(lib().moe_w4a16_down(self.handle, _ptr(a), T, topk, _ptr(routing), _ptr(out), _tuning(ovr),
                                    _stream(stream)))
         return out
@@ -345,7 +371,7 @@ class PreparedWeights:
     def dequant(self, which, expert, stream=None):
         import torch
         shape = (2 * self.I, self.H) if which == 13 else (self.H, self.I)
-        out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        out = _new(shape, torch.bfloat16, self.device, stream)
         check(lib().moe_dequant_weights(self.handle, which, expert, _ptr(out), _stream(stream)))
         return out
 
@@ -363,7 +389,7 @@ def swiglu(h, out=None, stream=None):
     import torch
     rows, two_i = h.shape
     if out is None:
-        out = torch.empty((rows, two_i // 2), dtype=torch.bfloat16, device=h.device)
+        out = _new((rows, two_i // 2), torch.bfloat16, h.device, stream)
     check(lib().moe_swiglu(_ptr(h), rows, two_i // 2, _ptr(out), _stream(stream)))
     return out
 
@@ -376,17 +402,6 @@ def swiglu(h, out=None, stream=None):
 # host needs for a call written carelessly: the helpers below look at every
 # tensor once, pass plain integers to the library and ask torch for the raw
 # stream.
-
-_torch = None
-_CODES = None       # torch dtype -> MOE_DTYPE_*
-
-
-def _load():
-    global _torch, _CODES
-    import torch
-    _CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
-    _torch = torch
-    return torch
 
 
 def _dtype(t) -> int:
@@ -435,21 +450,6 @@ def _dense(t, name, dtype, device, shape):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
     if not t.is_contiguous():
         raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: not contiguous")
-
-
-def _new(shape, dtype, device, stream):
-    """An output. For a stream other than the current one it is made on that
-    stream, because memory freed on the current one may still be in use by what
-    is queued there, and it is kept from reuse until both are done with it."""
-    torch = _torch
-    if stream is not None:
-        current = torch.cuda.current_stream(device)
-        if stream.cuda_stream != current.cuda_stream:
-            with torch.cuda.stream(stream):
-                t = torch.empty(*shape, dtype=dtype, device=device)
-            t.record_stream(current)
-            return t
-    return torch.empty(*shape, dtype=dtype, device=device)   # a tuple is read 0.1 us slower
 
 
 def _call(fn, device, stream, *args):
