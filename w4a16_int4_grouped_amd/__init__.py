@@ -455,6 +455,8 @@ def _dense(t, name, dtype, device, shape):
 def _call(fn, device, stream, *args):
     """fn(*args, stream) on `device`: on `stream`, or on its current stream."""
     torch = _torch
+    if stream is not None and stream.device_index != device.index:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"stream: on device {stream.device_index}, the operands on {device}")
     if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
