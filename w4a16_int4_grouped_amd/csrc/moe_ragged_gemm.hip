@@ -359,7 +359,10 @@ struct TileBody {
   // workgroups share a CU
   static constexpr int kPS = ONE ? 1 : NW == 4 ? 2 : MX ? (BJ > 192 ? 2 : 3) : BJ > 64 ? 3 : 4;
   static constexpr int kQS = ONE ? 1 : NW == 4 || BJ > 128 ? 2 : MX || BJ > 64 ? 3 : 4;
-  static constexpr int kPB = BI * kStageBytes, kQB = BJ * kStageBytes, kSB = MX ? (BI + BJ) * 16 : 0;
+  // a pair of steps' scales, 16 bytes a row of P and of Q: copied 64 rows at a time, so Q's 32 rows have room for 64
+  static constexpr int kScaleQ = (BJ + 63) / 64;   // copies
+  static constexpr int kPB = BI * kStageBytes, kQB = BJ * kStageBytes, kSB = MX ? BI * 16 + kScaleQ * 1024 : 0;
+  static_assert(!MX || BI % 64 == 0, "whole copies of P's scales");
   static constexpr int kPC = OpP::kCopies, kQC = OpQ::kCopies;
   static constexpr int kTurn = NW * 32 * (BI / WI * 4 + 16);   // what store() needs for FP32
   static constexpr int kRings = kPS * kPB + kQS * kQB + 2 * kSB, kLds = kRings > kTurn ? kRings : kTurn;
@@ -379,8 +382,8 @@ struct TileBody {
     for (int n = 0; n < BI / 64; n += NW)
       if (n + wave < BI / 64) copy16(ss + (n + wave) * 1024, prs, ((n + wave) * 64 + lane) * s_ld, s * 8);
 #pragma unroll
-    for (int n = 0; n < (BJ + 63) / 64; n += NW)
-      if (n + wave < (BJ + 63) / 64)
+    for (int n = 0; n < kScaleQ; n += NW)
+      if (n + wave < kScaleQ)
         copy16(ss + BI * 16 + (n + wave) * 1024, qrs, ((n + wave) * 64 + lane) * s_ld, s * 8);
   }
 
@@ -681,12 +684,13 @@ struct SplitBody {
   static constexpr int kVal = MX ? 256 : 64;
   using OpP = Operand<FMT, PC, BI, 1>;
   using OpQ = Operand<FMT, QC, BJ, 1>;
-  static constexpr int kSB = MX ? 2048 : 0;                        // 16 scales of up to 128 rows
+  static constexpr int kSB = MX ? 2048 : 0;                        // 16 scales of up to 64 rows of each operand
   static constexpr int kStage = (BI + BJ) * kStageBytes + kSB;
   static constexpr int kCopies = OpP::kCopies + OpQ::kCopies + (MX ? 2 : 0);
   static constexpr int kPitch = BI * 4 + 16, kSum = BJ * kPitch;   // a wave's sums
   static constexpr int kLds = W * (2 * kStage > kSum ? 2 * kStage : kSum);
   static_assert(kLds <= 160 * 1024, "LDS");
+  static_assert(BI <= 64 && BJ <= 64, "one copy of scales of each operand");
 
   __device__ __forceinline__ static void run(const RaggedParams& p, int e, const Group& g, int i0, int j0, int ni,
                                              int nj, char* all) {
