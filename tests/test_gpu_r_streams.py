@@ -76,3 +76,43 @@ def test_the_layer_does_not_reuse_the_current_streams_memory():
     assert not places & {o.data_ptr() for o, _ in got}
     for k, (a, b) in enumerate(got):
         assert torch.equal(a, want[k % 2]) and torch.equal(b, want[1 - k % 2]), k
+
+
+def test_side_stream_inside_a_capture():
+    """Outputs made for a side stream while a graph is captured belong to the graph: replays with eager calls of the
+    same sizes between them give the eager results."""
+    require_gpu()
+    import w4a16_int4_grouped_amd as M
+    log("case side stream in a capture")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    a, w1, w2, off = r(300, 256), r(3, 512, 256), r(3, 256, 512), offsets_of([100, 0, 200]).cuda()
+
+    def both(side):
+        """Two products on the side stream, a third of the caller's beside them."""
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream())
+        hid = M.grouped_gemm(a, w1, off, stream=side)
+        y = M.grouped_gemm(hid, w2, off, stream=side)
+        mine = M.grouped_gemm(a, w1, off, out_dtype=torch.float32)
+        if side is not None:
+            torch.cuda.current_stream().wait_stream(side)
+        return y + 1, mine
+
+    side = torch.cuda.Stream()
+    both(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both(side)
+    for k in range(4):
+        a.copy_(a.roll(1, 0))
+        want = both(None)
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        both(side if k % 2 else None)
+        torch.cuda.synchronize()
+        for x, y in zip(outs, want):
+            assert torch.equal(x, y), k
