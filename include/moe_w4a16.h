@@ -416,7 +416,9 @@ moe_status_t moe_swiglu(const uint16_t* h, int64_t rows, int32_t inter, uint16_t
  * were. Bounds are clamped to [0, M]; with offsets that decrease no memory
  * outside the arguments is touched, but the outputs are unspecified. The
  * offsets of a routing buffer (off_offsets) are such offsets for the rows
- * moe_permute writes.
+ * moe_permute writes; a group's padding (sentinel slots) belongs to it there:
+ * moe_permute writes 0 into those rows, and gradients given for them have to
+ * be finite, 0 if nothing else.
  *
  * Leading dimensions (ld) and strides count values of the matrix; ld is a
  * multiple of 8 and at most 2^21, pointers to matrices are 16-byte aligned.
@@ -436,7 +438,7 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
  *             the type)
  *   bias      device float [E] or NULL
  *   topk_ids  device int32 [T, topk], topk_w device float [T, topk]
- * E 1..4096, topk 1..min(E, 64). Errors: INVALID_ARG, HIP. */
+ * T 0..2^24, E 1..4096, topk 1..min(E, 64). Errors: INVALID_ARG, HIP. */
 moe_status_t moe_router_topk(const void* logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
                              int32_t topk, int32_t score, const float* bias, int32_t renorm,
                              float scale, int32_t* topk_ids, float* topk_w, moe_stream_t stream);
@@ -495,12 +497,13 @@ int32_t moe_mx_scale_cols(int32_t K);
  * above 6 to 6. A block that holds a NaN or an infinity becomes NaN (scale
  * byte 255, codes 0).
  *   x  device [rows, K] of dtype (BF16, FP16 or FP32), rows ld values apart,
- *      ld a multiple of 8
+ *      ld a multiple of 8; rows at most 2^40, rows * K at most 2^42
  * Errors: INVALID_ARG, HIP. */
 moe_status_t moe_mx_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32_t K,
                           uint8_t* q, uint8_t* scales, moe_stream_t stream);
 
-/* The values of MXFP4 rows, each rounded once to dtype. */
+/* The values of MXFP4 rows, each rounded once to dtype. Sizes and errors: as
+ * moe_mx_quant. */
 moe_status_t moe_mx_dequant(const uint8_t* q, const uint8_t* scales, int64_t rows, int32_t K,
                             void* out, int32_t dtype, int64_t ld, moe_stream_t stream);
 
