@@ -10,10 +10,13 @@
 //
 // Four lanes share a block, eight values each: 16-byte loads of 2-byte
 // values, 4-byte stores of codes, one byte of scale from the first. A
-// workgroup takes 1024 adjacent groups of 8, four a thread, so that all four
-// loads are in flight (98304 x 7168 BF16: 292 us, 6.1 TB/s read and written;
-// a fixed grid striding through memory took 410 us). HBM bounds it, as it
-// does the way back (340 us).
+// workgroup takes 1024 adjacent groups of 8, four a thread, so that the grid
+// passes through memory once (98304 x 7168 BF16: 310 us, 5.8 TB/s read and
+// written; a fixed grid striding through memory took 410 us). HBM bounds it, as
+// it does the way back (328 us). A thread's four loads do not cover for each
+// other where 16-bit values are unpacked under the load's condition: each is
+// waited for there, and the other waves of the CU are the cover; FP32 loads, and
+// the codes on the way back, are in flight together.
 #include "moe_device.h"
 #include "moe_ragged.h"
 
@@ -22,7 +25,7 @@ namespace {
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
-// Values are read once: past the caches (292 against 311 us for 1.4 GB).
+// Values are read once: past the caches (310 against 315 us for 1.4 GB).
 template <int TYPE>
 __device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) {
   if constexpr (TYPE == TYPE_F32) {
@@ -77,7 +80,7 @@ __device__ __forceinline__ void advance(Place& p, const Place& step, int n8) {
   if (p.c >= n8) p.c -= n8, ++p.r;
 }
 
-constexpr int kBatch = 4;   // groups per thread whose loads are in flight together
+constexpr int kBatch = 4;   // groups per thread
 
 template <int TYPE>
 __global__ __launch_bounds__(256) void mx_quant(const void* __restrict__ x, int64_t rows, int K8, int64_t ld,

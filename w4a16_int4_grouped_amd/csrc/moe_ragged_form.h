@@ -14,16 +14,42 @@ namespace moe {
 //   TWO    128 x 128, 4 waves, two a CU: 0.65 to 1.0 a step, 5 besides
 //   FOUR   the same in one LDS stage, four a CU that cover for each other: 0.95 to 2.0, 6 besides
 //   SPLIT  64 x 64, the contraction split over 4 waves: 0.75 for four steps, 4 besides
-//   THIN   32 x 64 over 6 waves (FP4: 5): 0.75 for six steps (0.5 on few CUs), 4 besides
-// Measured in us (rows in all, N, K):       LARGE   TWO  FOUR SPLIT  THIN
-//   48 experts, 24576, 4096, 7168            1467          2327
-//   384 experts, 32768, 7168, 256             517   514   409  2070
-//   16 experts, 8192, 2048, 1024               52    47    48   107
-//   1 expert, 1024, 4096, 4096                 74    47    68    59
-//   1 expert, 250, 4872, 7168                               46    55
-//   1 expert, 512, 512, 7168                  113    76   110    25    20
-//   1 expert, 64, 1024, 7168                                20    14
-//   wgrad, 64 experts, 4000, 2048, 2048       134   130   107   717
+//   THIN   32 x 64 over 6 waves (FP4: 5): 0.75 for six steps, 4 besides
+// The constants were fitted to the forward product; the gradients and FP4 use
+// them too. Measured in us, each form in turn on one GPU (rows in all, N, K; the
+// form taken is marked):
+//                                            LARGE    TWO   FOUR  SPLIT   THIN
+//   forward   48 experts, 24576, 4096, 7168  1412*   1696   2295   2832   4134
+//            384 experts, 32768, 7168, 256    483     448    363*  1684   2746
+//             16 experts,  8192, 2048, 1024    52*     47     49    106    154
+//             16 experts,  8192, 2048, 2048    92*     84     90    154    223
+//              1 expert,   1024, 4096, 4096    69      45*    63     57     90
+//              1 expert,    250, 4872, 7168   114      76    107     46*    55
+//              1 expert,    512,  512, 7168   114      76    108     24     19*
+//              1 expert,     64, 1024, 7168    50      42     52     20     14*
+//   input     48 experts, 24576, 4096, 7168  1440*   1684   2048   3119   5093
+//            384 experts, 32768, 256, 7168    490     474    380*  1711   2850
+//             16 experts,  8192, 2048, 1024    47      55*    50     80    124
+//             16 experts,  8192, 2048, 2048    94*     84     89    155    243
+//              1 expert,   1024, 4096, 4096    73      46*    63     58    104
+//              1 expert,    512, 7168, 512    120      74    103     28     26*
+//   weights    8 experts, 16384, 4096, 7168   884*   1002    971   1983   3246
+//             64 experts,  4000, 2048, 2048   150     128    107*   764   1133
+//             16 experts,  8192, 2048, 1024    48      50     45*   141    213
+//             16 experts,  2048,  512,  512    10       8.6*   9.3   14     20
+//              1 expert,   2000,  512,  512    42      17     24      9.4    8.9*
+//              1 expert,  24576,  256,  256   440     244    336     68     62*
+//   FP4       48 experts, 24576, 4096, 7168   487*    563    541   1193   1725
+//            384 experts, 32768, 7168, 256    288     284    201*  1462   2482
+//             16 experts,  8192, 2048, 2048    38      34     32*    89    129
+//              1 expert,   1024, 4096, 4096    27      16*    21     28     44
+//              1 expert,    250, 4872, 7168    39      24     33     20*    24
+//              1 expert,    512,  512, 7168    38      17     25     10      8.6*
+// Where the form taken is not the fastest (16 experts of 512 rows), estimates lie
+// within a few us of each other and the call loses 9 to 18 %.
+// The rule knows the rows in all, not the groups, which are on the device: it
+// takes a call as even over min(E, M) experts. A call whose rows lie with a few
+// of its experts gets the form of an even one.
 enum Form : int { LARGE = 0, TWO = 1, FOUR = 2, SPLIT = 3, THIN = 4 };
 
 // Waves that share a tile's contraction (SPLIT, THIN).

@@ -5,13 +5,15 @@
 // copies straight from global memory; each 16-byte fragment feeds a 32x32
 // matrix instruction, BF16 / FP16 (16 values of the contraction) and FP4 (64)
 // alike, so one kernel serves all. What bounds it:
-//   prefill (48 experts, 24576 rows, 4096 x 7168): 1420 us, 1.0 PFLOP/s where
-//     the library's plain product reaches 1.4 to 1.5; without the copies the
-//     same loop takes 1150: the rest is waiting for operands that miss the L2
-//     (6.5 GB for 3 GB of operands) and groups that end inside a tile and a
-//     round (9 and 10 %); FP4 470 us, 3.1 PFLOP/s
-//   decode (448 rows): the weights' bytes, 6.1 TB/s; FP4 5.6 TB/s
-//   short contractions (TP8 down, 256): the bytes, 5.2 TB/s
+//   prefill (48 experts, 24576 rows, 4096 x 7168): 1409 us, 1.0 PFLOP/s where
+//     the library's plain product of 16384 rows reaches 1.5 and this kernel 1.3
+//     on one expert; the same loop on operands that stay in LDS takes 960 (at
+//     the higher clock of operands that do not change): the rest is waiting for
+//     operands, which miss the L2 (7.0 GB for 3.2 GB of them), a tile's fill and
+//     store, with nothing beside it on its CU, and groups that end inside a tile
+//     and a round (5 and 7 %); FP4 474 us, 3.0 PFLOP/s
+//   decode (448 rows): the weights' bytes, 6.2 TB/s; FP4 5.6 TB/s
+//   short contractions (TP8 down, 256): the bytes, 5.1 TB/s
 #include <type_traits>
 
 #include "moe_device.h"
@@ -764,7 +766,7 @@ struct SplitBody {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read
       if (k + 2 < mine) issue(k + 2);
     }
-    // the sums as rows j of 64 values i
+    // the sums as rows j of BI values i
 #pragma unroll
     for (int u = 0; u < TJ; ++u)
 #pragma unroll

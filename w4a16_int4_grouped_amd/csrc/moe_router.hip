@@ -11,11 +11,14 @@
 // (sigmoid), which neither overflows nor divides by zero.
 //
 // One wave per token: each lane holds the keys of experts lane, lane + 64,
-// ..; a round takes each lane's best, then the wave's. The k rounds depend on
-// each other, so latency bounds small T: the wave's best comes by six DPP
-// steps (lane exchanges through LDS: 10.4 us for one token of 384 experts
-// with a bias, against 6.1). The rounds' instructions bound large T (8192
-// tokens of 384 experts in BF16, top-8: 7.8 us; 65536: 45 us).
+// ..; a round takes each lane's best, then the wave's. Latency bounds small T:
+// the k rounds depend on each other, and before them a lane's loads do not
+// overlap, because the conversion (and the bias) stands under the load's
+// condition: 64 experts take 3.4 us, 384 take 6.0 (one token in FP32 with a
+// bias, top-8). The wave's best comes by six DPP steps (lane exchanges through
+// LDS: 10.4 us for the token of 384 experts). The rounds' instructions, which go
+// over all of a lane's keys, bound large T (8192 tokens of 384 experts in BF16,
+// top-8: 8.0 us; 65536: 46 us).
 #include <type_traits>
 
 #include "moe_device.h"
@@ -155,7 +158,8 @@ enum KeyKind : int { KEY16 = 0, KEY32 = 1, KEYB = 2 };
 __device__ __forceinline__ uint32_t ordered(uint32_t b) { return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u); }
 __device__ __forceinline__ uint32_t unordered(uint32_t s) { return s ^ (s >> 31 ? 0x80000000u : 0xFFFFFFFFu); }
 
-// VPL: experts per lane.
+// VPL: places for experts per lane, kept in registers; those past E cost their
+// instructions all the same.
 template <int TYPE, int VPL, int KIND>
 __global__ __launch_bounds__(256) void router_topk(RouterParams p) {
   const int lane = threadIdx.x & 63;
@@ -295,9 +299,12 @@ __global__ __launch_bounds__(256) void router_topk(RouterParams p) {
 // part; an id given twice adds up.
 // One wave per token; a lane writes V adjacent experts at a time (V = 8, 16
 // bytes and more, where rows allow it). The chosen experts' values are put in
-// their places of 64 V zeros in LDS: 5.1 us for 8192 tokens of 384 experts, 7.1
-// for 2000 of 4096, top-32 (k comparisons for each of a lane's experts: 7.0 and
-// 30). The bytes bound the large rows, the wave's instructions the small.
+// their places of 64 V zeros in LDS: side by side 5.1 us for 8192 tokens of 384
+// experts, 7.1 for 2000 of 4096, top-32 (k comparisons for each of a lane's
+// experts: 7.0 and 30). The bytes bound the large rows, the wave's instructions
+// the small. The softmax's own gradient (no renorm) reads its row three times,
+// twice a value a lane at a time: 12.3 us for 8192 tokens of 384, 87 for 8192 of
+// 4096, top-32, where the bytes take 2.5 and 27.
 template <int TYPE, int V>
 __global__ __launch_bounds__(256) void router_topk_grad(RouterParams p) {
   const int lane = threadIdx.x & 63;
@@ -380,6 +387,15 @@ __global__ __launch_bounds__(256) void router_topk_grad(RouterParams p) {
   }
 }
 
+// Places by E, in kernel us for 8192 tokens, top-8 (BF16 softmax / FP32 sigmoid
+// with a bias), at both ends of each step:
+//   1    up to 64      5.2 / 11
+//   4    65 .. 256     6.6 / 14   ..  6.9 / 16
+//   6    257 .. 384    7.8 / 19   ..  8.0 / 20
+//   16   385 .. 1024    13 / 33   ..   14 / 44
+//   64   1025 .. 4096   37 / 221  ..   69 / 381
+// A step costs most just past its border: 385 experts take 16 places where 7
+// would do, 1025 take 64 where 17 would.
 template <int TYPE, int KIND>
 hipError_t topk_for(const RouterParams& p, hipStream_t s) {
   const unsigned g = (unsigned)((p.T + 3) / 4);
