@@ -2,8 +2,6 @@
 // arithmetic on a call's sizes.
 #pragma once
 
-#include <stdint.h>
-
 namespace moe {
 
 // The forms of tiles, and which a call takes: the one whose estimate is the
