@@ -518,6 +518,144 @@ moe_status_t moe_mx_grouped_gemm(const uint8_t* aq, const uint8_t* a_scales, con
                                  int32_t M, int32_t N, int32_t K, void* out, int64_t out_ld,
                                  int32_t out_dtype, moe_stream_t stream);
 
+/* ---- operators of a training step -------------------------------------------
+ *
+ * What lies between the router, the experts' products and their gradients.
+ * Conventions as for the operators above; row counts and offsets too. Sums are
+ * held in FP32 or FP64 in a fixed order: a call's results are the same bits
+ * every time. */
+
+/* Bytes of moe_router_balance's workspace for T tokens, E experts and S
+ * sequences (limits there), 0 for others. */
+size_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S);
+
+/* Rows per expert and the load-balance loss of each sequence of tokens.
+ * Sequence s holds the n rows [offsets[s], offsets[s + 1]) (device int32
+ * [S + 1], not decreasing, clamped to [0, T]; NULL with S = 1: all rows):
+ *   counts[s][e]  how often topk_ids names e in its rows (ids outside [0, E)
+ *                 count nowhere)
+ *   loss[s]       E * sum over e of (counts / (n topk)) * (sum of p / n), 0
+ *                 for a sequence without rows
+ * with p the softmax of a row's logits, or their sigmoids over the sigmoids'
+ * sum. A logit of -inf or NaN has p = 0, +inf counts as the largest FP32 value;
+ * a row without other logits adds nothing to the sum of p.
+ *   logits    device [T, E] of dtype, rows ld values apart (any alignment of
+ *             the type); topk_ids device int32 [T, topk]
+ *   loss      device float [S], counts device int32 [S, E], fully written
+ *   ws        device, 16-byte aligned, of ws_bytes >= moe_router_balance_bytes;
+ *             nothing in it has to be kept or cleared between calls
+ * T 0..2^24, E 1..4096, topk 1..min(E, 64), S 1..2^20, S * E up to 2^30.
+ * Enqueues up to two kernels. Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, HIP. */
+moe_status_t moe_router_balance(const void* logits, int32_t dtype, int64_t ld, int32_t T,
+                                int32_t E, const int32_t* topk_ids, int32_t topk, int32_t score,
+                                const int32_t* offsets, int32_t S, float* loss, int32_t* counts,
+                                void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of the logits for the gradient d_loss (device float [S]) of the
+ * losses and the counts moe_router_balance wrote (which have none): with
+ * c = d_loss E counts / (n^2 topk), d_logits = p (c - sum over e of c p), for
+ * sigmoid scores times 1 - sigmoid(logit); 0 for rows of no sequence.
+ *   add       device [T, E] of dtype, rows add_ld values apart: added before
+ *             the one rounding (moe_router_topk_grad's result); may be d_logits
+ *             itself; or NULL
+ *   d_logits  device [T, E] of dtype, rows d_ld values apart, fully written
+ * Limits and errors: as moe_router_balance. */
+moe_status_t moe_router_balance_grad(const void* logits, int32_t dtype, int64_t ld, int32_t T,
+                                     int32_t E, int32_t topk, int32_t score,
+                                     const int32_t* offsets, int32_t S, const int32_t* counts,
+                                     const float* d_loss, const void* add, int64_t add_ld,
+                                     void* d_logits, int64_t d_ld, moe_stream_t stream);
+
+/* A token's sum of rows: out[t] = sum over j of w[t][j] * y[slots[t][j]], in
+ * FP32 in ascending j, rounded once. A slot outside [0, R) names no row and
+ * adds nothing; a token without rows gets 0. The off_slot_of section of a
+ * routing buffer holds such slots. With w NULL (1 each) it is the gradient of
+ * moe_permute's input.
+ *   y      device [R, H] of dtype (BF16, FP16 or FP32)
+ *   slots  device int32 [T, topk], w device float [T, topk] or NULL
+ *   out    device [T, H] of out_dtype
+ * H is a multiple of 8 up to 2^20, T 0..2^24, topk 1..64, R up to 2^30.
+ * Errors: INVALID_ARG, HIP. */
+moe_status_t moe_combine(const void* y, int32_t dtype, int64_t y_ld, int32_t R, int32_t H,
+                         const int32_t* slots, int32_t T, int32_t topk, const float* w, void* out,
+                         int64_t out_ld, int32_t out_dtype, moe_stream_t stream);
+
+/* Gradients of moe_combine for the gradient d_out (device [T, H] of dtype):
+ *   d_y[slots[t][j]] = w[t][j] * d_out[t]      device [R, H] of dtype
+ *   d_w[t][j] = <d_out[t], y[slots[t][j]]>     device float [T, topk], 0 where
+ *               the slot names no row; NULL: not computed, y is not read
+ * A row is named by one slot at most, as in a routing (a row named twice holds
+ * one of its gradients, or parts of both). Rows that no slot names are left as
+ * they were, but with
+ *   row_src    device int32 [R] (the off_sorted section of a routing buffer),
+ *              every row of [offsets[0], offsets[E]) (offsets NULL: of all R)
+ *              whose row_src lies outside [0, T * topk) is written 0: a group's
+ *              padding, as the gradients of grouped products need it
+ * Limits and errors: as moe_combine, E 1..4096. */
+moe_status_t moe_combine_grad(const void* d_out, int32_t dtype, int64_t d_ld, int32_t T, int32_t H,
+                              const int32_t* slots, int32_t topk, const float* w, const void* y,
+                              int64_t y_ld, const int32_t* row_src, const int32_t* offsets,
+                              int32_t E, void* d_y, int64_t dy_ld, int32_t R, float* d_w,
+                              moe_stream_t stream);
+
+/* Rows of K values in 8 bits (MXINT8; K a multiple of 8): codes int8 [rows, K]
+ * and scales uint8 [rows, moe_mx8_scale_cols(K)], one E8M0 byte (2^(byte -
+ * 127), 255 = NaN) per 32 values (a row's last block may be shorter), a row
+ * padded to a multiple of 16 bytes (written as 0, read as nothing). A value is
+ * code * 2^(byte - 133). Both are dense. 0 for a bad K. */
+int32_t moe_mx8_scale_cols(int32_t K);
+
+/* Rows in 8 bits. A block's scale is 2^floor(log2 m) for its largest magnitude
+ * m (at least 2^-127); codes are rounded to nearest even and end at -127 and
+ * 127. They are exact in BF16, FP16 (within its range) and FP32. A block that
+ * holds a NaN or an infinity becomes NaN (scale byte 255, codes 0).
+ *   x  device [rows, K] of dtype (BF16, FP16 or FP32), rows ld values apart;
+ *      rows at most 2^40, rows * K at most 2^42
+ * Errors: INVALID_ARG, HIP. */
+moe_status_t moe_mx8_quant(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32_t K,
+                           int8_t* q, uint8_t* scales, moe_stream_t stream);
+
+/* The values of rows in 8 bits, each rounded once to dtype: out[r] is row r,
+ * or with row_src (device int32 [out_rows]) row row_src[r] / topk (0 where
+ * row_src[r] lies outside [0, rows * topk)): of a routing buffer's off_sorted
+ * section and its topk, the rows moe_permute would write. With offsets (device
+ * int32 [E + 1]) only rows [offsets[0], offsets[E]) are written.
+ *   out  device [out_rows, K] of dtype, rows ld values apart; out_rows = rows
+ *        without row_src; up to 2^30 rows with it
+ * Otherwise as moe_mx8_quant, E 1..4096. */
+moe_status_t moe_mx8_dequant(const int8_t* q, const uint8_t* scales, int64_t rows, int32_t K,
+                             const int32_t* row_src, int32_t topk, const int32_t* offsets,
+                             int32_t E, void* out, int32_t dtype, int64_t ld, int64_t out_rows,
+                             moe_stream_t stream);
+
+/* SwiGLU that keeps its input in 8 bits: a[r][c] = silu(g) * u with g =
+ * h[r][c], u = h[r][inter + c], and g and u as moe_mx8_quant would write them
+ * for the 2 * rows rows of inter values (each half in blocks of its own).
+ *   h       device [rows, 2 * inter] of dtype, a device [rows, inter] of dtype
+ *   q       device int8 [rows, 2, inter]
+ *   scales  device uint8 [rows, 2, moe_mx8_scale_cols(inter)]
+ *   offsets device int32 [E + 1] or NULL: only rows [offsets[0], offsets[E])
+ *           are read and written
+ * inter is a multiple of 8 up to 2^19, rows up to 2^30, E 1..4096. Errors:
+ * INVALID_ARG, HIP. */
+moe_status_t moe_swiglu_save(const void* h, int32_t dtype, int64_t h_ld, int32_t rows,
+                             int32_t inter, const int32_t* offsets, int32_t E, void* a,
+                             int64_t a_ld, int8_t* q, uint8_t* scales, moe_stream_t stream);
+
+/* Gradient of SwiGLU's input for the gradient d_a of its output, and the output
+ * again: with s = sigmoid(g),
+ *   d_h[r][c] = d_a u s (1 + g (1 - s)), d_h[r][inter + c] = d_a g s,
+ *   a[r][c] = g s u
+ * for g and u from h (device [rows, 2 * inter] of dtype), or with h NULL the
+ * values of q and scales as moe_swiglu_save wrote them.
+ *   d_a  device [rows, inter], d_h device [rows, 2 * inter], a device [rows,
+ *        inter] or NULL, all of dtype
+ * offsets, limits and errors: as moe_swiglu_save. */
+moe_status_t moe_swiglu_grad(const void* h, int64_t h_ld, const int8_t* q, const uint8_t* scales,
+                             int32_t dtype, int32_t rows, int32_t inter, const void* d_a,
+                             int64_t da_ld, const int32_t* offsets, int32_t E, void* d_h,
+                             int64_t dh_ld, void* a, int64_t a_ld, moe_stream_t stream);
+
 /* ---- inspection ------------------------------------------------------------ */
 
 /* Dequantise one expert's prepared matrix back to canonical order with the

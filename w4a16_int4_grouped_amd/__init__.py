@@ -51,6 +51,8 @@ EXPORTS = [
     "moe_router_topk", "moe_router_topk_grad", "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
     "moe_mx_scale_cols", "moe_mx_quant", "moe_mx_dequant", "moe_mx_grouped_gemm",
     "moe_profile_enable", "moe_profile_reset", "moe_profile_read",
+    "moe_router_balance_bytes", "moe_router_balance", "moe_router_balance_grad", "moe_combine", "moe_combine_grad",
+    "moe_mx8_scale_cols", "moe_mx8_quant", "moe_mx8_dequant", "moe_swiglu_save", "moe_swiglu_grad",
 ]
 
 
@@ -136,6 +138,16 @@ def lib() -> ctypes.CDLL:
         "moe_mx_quant": (S, [P, I32, I64, I64, I32, P, P, P]),
         "moe_mx_dequant": (S, [P, P, I64, I32, P, I32, I64, P]),
         "moe_mx_grouped_gemm": (S, [P, P, P, P, P, I32, I32, I32, I32, P, I64, I32, P]),
+        "moe_router_balance_bytes": (SZ, [I32, I32, I32]),
+        "moe_router_balance": (S, [P, I32, I64, I32, I32, P, I32, I32, P, I32, P, P, P, SZ, P]),
+        "moe_router_balance_grad": (S, [P, I32, I64, I32, I32, I32, I32, P, I32, P, P, P, I64, P, I64, P]),
+        "moe_combine": (S, [P, I32, I64, I32, I32, P, I32, I32, P, P, I64, I32, P]),
+        "moe_combine_grad": (S, [P, I32, I64, I32, I32, P, I32, P, P, I64, P, P, I32, P, I64, I32, P, P]),
+        "moe_mx8_scale_cols": (I32, [I32]),
+        "moe_mx8_quant": (S, [P, I32, I64, I64, I32, P, P, P]),
+        "moe_mx8_dequant": (S, [P, P, I64, I32, P, I32, P, I32, P, I32, I64, I64, P]),
+        "moe_swiglu_save": (S, [P, I32, I64, I32, I32, P, I32, P, I64, P, P, P]),
+        "moe_swiglu_grad": (S, [P, I64, P, P, I32, I32, I32, P, I64, P, I32, P, I64, P, I64, P]),
         "moe_profile_enable": (S, [S]),
         "moe_profile_reset": (None, []),
         "moe_profile_read": (S, [ctypes.c_char_p, SZ]),
@@ -690,6 +702,295 @@ def mx_grouped_gemm(aq, a_scales, wq, w_scales, offsets, out=None, out_dtype=Non
           aq.data_ptr(), a_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), E, M, N, K,
           out.data_ptr(), o_ld, _dtype(out.dtype))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Operators of a training step around the experts' products
+# ---------------------------------------------------------------------------
+
+
+def _score(score) -> int:
+    code = SCORES.get(score)
+    if code is None:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"score {score!r}: softmax or sigmoid")
+    return code
+
+
+def _offsets(t, device):
+    """(pointer, count - 1) of int32 offsets, or (None, 0)."""
+    if t is None:
+        return None, 0
+    _need(t.dim() == 1 and t.shape[0] >= 2, "offsets: [E + 1]")
+    _dense(t, "offsets", _torch.int32, device, tuple(t.shape))
+    return t.data_ptr(), t.shape[0] - 1
+
+
+def router_balance(logits, ids, score="softmax", offsets=None, out=None, ws=None, stream=None):
+    """(loss float32 [S], counts int32 [S, E]) of S sequences of tokens, rows
+    [offsets[s], offsets[s + 1]) of logits [T, E] (bf16, fp16 or fp32) and of
+    their chosen experts ids (int32 [T, topk]); without offsets one sequence of
+    all rows. counts: how often a sequence chose each expert. loss: E * sum_e
+    f_e P_e with the shares f of the choices and the mean scores P (softmax, or
+    sigmoids over their sum); 0 for an empty sequence. Ids outside [0, E) count
+    nowhere, a logit of -inf or NaN has score 0. `out` may give the two tensors,
+    `ws` a uint8 workspace."""
+    torch = _torch or _load()
+    _need(logits.dim() == 2 and ids.dim() == 2, "logits: [T, E], ids: [T, topk]")
+    T, E = logits.shape
+    topk = ids.shape[1]
+    ld = _matrix(logits, "logits")
+    dev = logits.device
+    _fits(T | E | topk)
+    _dense(ids, "ids", torch.int32, dev, (T, topk))
+    off, S = (None, 1) if offsets is None else _offsets(offsets, dev)
+    L = _lib or lib()
+    if out is None:
+        loss = _new((S,), torch.float32, dev, stream)
+        counts = _new((S, E), torch.int32, dev, stream)
+    else:
+        loss, counts = out
+        _dense(loss, "loss", torch.float32, dev, (S,))
+        _dense(counts, "counts", torch.int32, dev, (S, E))
+    if ws is None:
+        nbytes = L.moe_router_balance_bytes(T, E, S)
+        if nbytes == 0:
+            check(MOE_ERR_INVALID_ARG)
+        ws = _empty(nbytes, dev, stream)
+    else:
+        nbytes = ws.numel()
+        _dense(ws, "ws", torch.uint8, dev, (nbytes,))
+    _call(L.moe_router_balance, dev, stream,
+          logits.data_ptr(), _dtype(logits.dtype), ld, T, E, ids.data_ptr(), topk, _score(score), off, S,
+          loss.data_ptr(), counts.data_ptr(), ws.data_ptr(), nbytes)
+    return loss, counts
+
+
+def router_balance_grad(logits, counts, d_loss, topk, score="softmax", offsets=None, add=None, out=None, stream=None):
+    """Gradient [T, E] of the logits (their dtype) for the gradient d_loss
+    (float32 [S]) of router_balance's losses, with the counts that it returned;
+    0 for rows of no sequence. `add` [T, E] (router_topk_grad's result, of the
+    logits' dtype) is added before the one rounding; it may be `out` itself."""
+    torch = _torch or _load()
+    _need(logits.dim() == 2, "logits: [T, E]")
+    T, E = logits.shape
+    ld = _matrix(logits, "logits")
+    dev = logits.device
+    _need(topk >= 1, "topk: at least 1")
+    _fits(T | E | topk)
+    off, S = (None, 1) if offsets is None else _offsets(offsets, dev)
+    _dense(counts, "counts", torch.int32, dev, (S, E))
+    _dense(d_loss, "d_loss", torch.float32, dev, (S,))
+    a_ld = 0 if add is None else _matrix(add, "add", logits.dtype, dev, (T, E))
+    if out is None:
+        out = _new((T, E), logits.dtype, dev, stream)
+        o_ld = E
+    else:
+        o_ld = _matrix(out, "out", logits.dtype, dev, (T, E))
+    _call((_lib or lib()).moe_router_balance_grad, dev, stream,
+          logits.data_ptr(), _dtype(logits.dtype), ld, T, E, topk, _score(score), off, S, counts.data_ptr(),
+          d_loss.data_ptr(), None if add is None else add.data_ptr(), a_ld, out.data_ptr(), o_ld)
+    return out
+
+
+def combine(y, slots, w=None, out=None, out_dtype=None, stream=None):
+    """out[t] = sum_j w[t, j] * y[slots[t, j]] in FP32, j ascending, [T, H] of
+    out_dtype (default y's): a token's routed rows. y [R, H] bf16, fp16 or fp32
+    (H a multiple of 8), slots int32 [T, topk] (a slot outside [0, R), as -1,
+    names no row), w float32 [T, topk] or None for 1: the gradient of a
+    permutation's input. A routing buffer's slot_of section holds such slots."""
+    torch = _torch or _load()
+    _need(y.dim() == 2 and slots.dim() == 2, "y: [R, H], slots: [T, topk]")
+    R, H = y.shape
+    T, topk = slots.shape
+    _fits(R | H | T | topk)
+    y_ld = _matrix(y, "y")
+    dev = y.device
+    _dense(slots, "slots", torch.int32, dev, (T, topk))
+    if w is not None:
+        _dense(w, "w", torch.float32, dev, (T, topk))
+    if out is None:
+        out = _new((T, H), out_dtype or y.dtype, dev, stream)
+        o_ld = H
+    else:
+        o_ld = _matrix(out, "out", out_dtype, dev, (T, H))
+    _call((_lib or lib()).moe_combine, dev, stream,
+          y.data_ptr(), _dtype(y.dtype), y_ld, R, H, slots.data_ptr(), T, topk, None if w is None else w.data_ptr(),
+          out.data_ptr(), o_ld, _dtype(out.dtype))
+    return out
+
+
+def combine_grad(d_out, slots, y=None, w=None, row_src=None, offsets=None, out=None, stream=None):
+    """(d_y [R, H], d_w float32 [T, topk]) for the gradient d_out [T, H] of
+    combine's result: d_y[slots[t, j]] = w[t, j] * d_out[t], d_w[t, j] =
+    <d_out[t], y[slots[t, j]]> (None without y). A row is named by one slot at
+    most. R is y's, or row_src's, or that of the d_y in `out` = (d_y, d_w or
+    None). Rows that no slot names stay as they are (unspecified in a new d_y),
+    but with row_src (int32 [R], a routing buffer's sorted_ids section: t * topk
+    + j of each row) the rows of [offsets[0], offsets[-1]) whose row_src lies
+    outside [0, T * topk) become 0, which grouped products need in a group's
+    padding; without offsets those of all R."""
+    torch = _torch or _load()
+    _need(d_out.dim() == 2 and slots.dim() == 2, "d_out: [T, H], slots: [T, topk]")
+    T, H = d_out.shape
+    topk = slots.shape[1]
+    d_ld = _matrix(d_out, "d_out")
+    dev = d_out.device
+    _dense(slots, "slots", torch.int32, dev, (T, topk))
+    if w is not None:
+        _dense(w, "w", torch.float32, dev, (T, topk))
+    d_y, d_w = (None, None) if out is None else out
+    like = y if y is not None else row_src if row_src is not None else d_y
+    _need(like is not None, "one of y, row_src and out gives the number of rows")
+    R = like.shape[0]
+    _fits(R | H | T | topk)
+    y_ld = 0 if y is None else _matrix(y, "y", d_out.dtype, dev, (R, H))
+    if row_src is not None:
+        _dense(row_src, "row_src", torch.int32, dev, (R,))
+    _need(offsets is None or row_src is not None, "offsets without row_src")
+    off, E = _offsets(offsets, dev)
+    if d_y is None:
+        d_y = _new((R, H), d_out.dtype, dev, stream)
+        dy_ld = H
+    else:
+        dy_ld = _matrix(d_y, "d_y", d_out.dtype, dev, (R, H))
+    if d_w is not None:
+        _need(y is not None, "d_w without y")
+        _dense(d_w, "d_w", torch.float32, dev, (T, topk))
+    elif y is not None:
+        d_w = _new((T, topk), torch.float32, dev, stream)
+    _call((_lib or lib()).moe_combine_grad, dev, stream,
+          d_out.data_ptr(), _dtype(d_out.dtype), d_ld, T, H, slots.data_ptr(), topk, None if w is None else w.data_ptr(),
+          None if y is None else y.data_ptr(), y_ld, None if row_src is None else row_src.data_ptr(), off, E,
+          d_y.data_ptr(), dy_ld, R, None if d_w is None else d_w.data_ptr())
+    return d_y, d_w
+
+
+@functools.lru_cache(maxsize=None)
+def mx8_scale_cols(K) -> int:
+    """Bytes of a row of 8-bit rows' scales: K / 32 rounded up, then to a multiple of 16."""
+    _fits(K)
+    n = lib().moe_mx8_scale_cols(K)
+    if n == 0:
+        check(MOE_ERR_INVALID_ARG)
+    return n
+
+
+def mx8_quant(x, out=None, stream=None):
+    """Rows of x [rows, K] (bf16, fp16 or fp32, K a multiple of 8) in 8 bits:
+    (codes int8 [rows, K], scales uint8 [rows, mx8_scale_cols(K)], one E8M0 byte
+    per 32 values). A value is code * 2^(byte - 133), within a 128th of its
+    block's largest magnitude, and exact in bf16; a block with a NaN or an
+    infinity becomes NaN. `out` may give the two tensors."""
+    torch = _torch or _load()
+    _need(x.dim() == 2, "x: [rows, K]")
+    rows, K = x.shape
+    ld = _matrix(x, "x")
+    cols = mx8_scale_cols(K)
+    dev = x.device
+    if out is None:
+        q = _new((rows, K), torch.int8, dev, stream)
+        scales = _new((rows, cols), torch.uint8, dev, stream)
+    else:
+        q, scales = out
+        _dense(q, "codes", torch.int8, dev, (rows, K))
+        _dense(scales, "scales", torch.uint8, dev, (rows, cols))
+    _call((_lib or lib()).moe_mx8_quant, dev, stream,
+          x.data_ptr(), _dtype(x.dtype), ld, rows, K, q.data_ptr(), scales.data_ptr())
+    return q, scales
+
+
+def mx8_dequant(q, scales, dtype=None, row_src=None, topk=1, offsets=None, out=None, stream=None):
+    """Values of rows in 8 bits in `dtype` (default bf16): [rows, K], or with
+    row_src (int32 [R]) [R, K] of rows row_src[r] // topk, 0 where row_src[r]
+    lies outside [0, rows * topk). With a routing buffer's sorted_ids as row_src
+    these are the rows that `permute` writes. With offsets (int32 [E + 1]) only
+    rows [offsets[0], offsets[-1]) are written."""
+    torch = _torch or _load()
+    _need(q.dim() == 2, "codes: [rows, K]")
+    rows, K = q.shape
+    dev = q.device
+    _dense(q, "codes", torch.int8, dev, (rows, K))
+    _dense(scales, "scales", torch.uint8, dev, (rows, mx8_scale_cols(K)))
+    R = rows
+    if row_src is not None:
+        _need(row_src.dim() == 1 and topk >= 1, "row_src: [R], topk: at least 1")
+        R = row_src.shape[0]
+        _dense(row_src, "row_src", torch.int32, dev, (R,))
+        _fits(R | rows | topk)
+    off, E = _offsets(offsets, dev)
+    if out is None:
+        out = _new((R, K), dtype or torch.bfloat16, dev, stream)
+        ld = K
+    else:
+        ld = _matrix(out, "out", dtype, dev, (R, K))
+    _call((_lib or lib()).moe_mx8_dequant, dev, stream,
+          q.data_ptr(), scales.data_ptr(), rows, K, None if row_src is None else row_src.data_ptr(), topk, off, E,
+          out.data_ptr(), _dtype(out.dtype), ld, R)
+    return out
+
+
+def swiglu_save(h, offsets=None, out=None, stream=None):
+    """(a [rows, I], codes int8 [rows, 2, I], scales uint8 [rows, 2,
+    mx8_scale_cols(I)]): a = silu(h[:, :I]) * h[:, I:] of h [rows, 2I] (bf16,
+    fp16 or fp32, I a multiple of 8), and h in 8 bits for swiglu_grad, as
+    mx8_quant writes the 2 * rows rows of I values. With offsets (int32 [E + 1])
+    only rows [offsets[0], offsets[-1]) are read and written. `out` may give the
+    three tensors."""
+    torch = _torch or _load()
+    _need(h.dim() == 2 and h.shape[1] % 2 == 0, "h: [rows, 2I]")
+    rows, I = h.shape[0], h.shape[1] // 2
+    _fits(rows | I)
+    ld = _matrix(h, "h")
+    cols = mx8_scale_cols(I)
+    dev = h.device
+    off, E = _offsets(offsets, dev)
+    if out is None:
+        a = _new((rows, I), h.dtype, dev, stream)
+        q = _new((rows, 2, I), torch.int8, dev, stream)
+        scales = _new((rows, 2, cols), torch.uint8, dev, stream)
+        a_ld = I
+    else:
+        a, q, scales = out
+        a_ld = _matrix(a, "a", h.dtype, dev, (rows, I))
+        _dense(q, "codes", torch.int8, dev, (rows, 2, I))
+        _dense(scales, "scales", torch.uint8, dev, (rows, 2, cols))
+    _call((_lib or lib()).moe_swiglu_save, dev, stream,
+          h.data_ptr(), _dtype(h.dtype), ld, rows, I, off, E, a.data_ptr(), a_ld, q.data_ptr(), scales.data_ptr())
+    return a, q, scales
+
+
+def swiglu_grad(h, d_a, scales=None, offsets=None, need_a=True, out=None, stream=None):
+    """(d_h [rows, 2I], a [rows, I]) of d_a's dtype for the gradient d_a
+    [rows, I] of a = silu(g) * u: the gradient of h = g | u, and a once more
+    (None without need_a). h is [rows, 2I] of d_a's dtype, or with scales the
+    codes int8 [rows, 2, I] that swiglu_save returned. With offsets (int32
+    [E + 1]) only rows [offsets[0], offsets[-1]) are read and written. `out` may
+    give the two tensors."""
+    torch = _torch or _load()
+    _need(d_a.dim() == 2, "d_a: [rows, I]")
+    rows, I = d_a.shape
+    _fits(rows | I)
+    da_ld = _matrix(d_a, "d_a")
+    dev = d_a.device
+    off, E = _offsets(offsets, dev)
+    if scales is None:
+        h_at, h_ld, q_at, s_at = h.data_ptr(), _matrix(h, "h", d_a.dtype, dev, (rows, 2 * I)), None, None
+    else:
+        _dense(h, "codes", torch.int8, dev, (rows, 2, I))
+        _dense(scales, "scales", torch.uint8, dev, (rows, 2, mx8_scale_cols(I)))
+        h_at, h_ld, q_at, s_at = None, 0, h.data_ptr(), scales.data_ptr()
+    if out is None:
+        d_h = _new((rows, 2 * I), d_a.dtype, dev, stream)
+        a = _new((rows, I), d_a.dtype, dev, stream) if need_a else None
+        dh_ld, a_ld = 2 * I, I
+    else:
+        d_h, a = out
+        dh_ld = _matrix(d_h, "d_h", d_a.dtype, dev, (rows, 2 * I))
+        a_ld = 0 if a is None else _matrix(a, "a", d_a.dtype, dev, (rows, I))
+    _call((_lib or lib()).moe_swiglu_grad, dev, stream,
+          h_at, h_ld, q_at, s_at, _dtype(d_a.dtype), rows, I, d_a.data_ptr(), da_ld, off, E, d_h.data_ptr(), dh_ld,
+          None if a is None else a.data_ptr(), a_ld)
+    return d_h, a
 
 
 def profile_enable(on=True):

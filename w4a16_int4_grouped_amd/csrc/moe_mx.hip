@@ -17,68 +17,11 @@
 // other where 16-bit values are unpacked under the load's condition: each is
 // waited for there, and the other waves of the CU are the cover; FP32 loads, and
 // the codes on the way back, are in flight together.
-#include "moe_device.h"
 #include "moe_ragged.h"
+#include "moe_rows.h"
 
 namespace moe {
 namespace {
-
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-
-// Values are read once: past the caches (310 against 315 us for 1.4 GB).
-template <int TYPE>
-__device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) {
-  if constexpr (TYPE == TYPE_F32) {
-    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(x) + at);
-    const f32x4_t a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-  } else {
-    const u32x4_t w =
-        __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(x) + at));
-    if constexpr (TYPE == TYPE_BF16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
-    } else {
-      const f16x8_t h = __builtin_bit_cast(f16x8_t, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
-    }
-  }
-}
-
-template <int TYPE>
-__device__ __forceinline__ void store8(void* x, int64_t at, const float (&v)[8]) {
-  if constexpr (TYPE == TYPE_F32) {
-    f32x4_t* p = reinterpret_cast<f32x4_t*>(static_cast<float*>(x) + at);
-    p[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-    p[1] = f32x4_t{v[4], v[5], v[6], v[7]};
-  } else if constexpr (TYPE == TYPE_BF16) {
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(x) + at) =
-        u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-  } else {
-    f16x8_t h;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
-    *reinterpret_cast<f16x8_t*>(static_cast<_Float16*>(x) + at) = h;
-  }
-}
-
-// A thread's places among rows of n8 groups of 8 values: its first by one
-// division, the next ones a workgroup's 256 groups on by additions.
-struct Place {
-  int64_t r;
-  int c;
-};
-__device__ __forceinline__ Place place_of(int64_t i, int n8) {
-  const int64_t r = i / n8;
-  return Place{r, (int)(i - r * n8)};
-}
-__device__ __forceinline__ void advance(Place& p, const Place& step, int n8) {
-  p.r += step.r;
-  p.c += step.c;
-  if (p.c >= n8) p.c -= n8, ++p.r;
-}
 
 constexpr int kBatch = 4;   // groups per thread
 

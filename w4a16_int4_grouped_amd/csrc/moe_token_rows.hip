@@ -1,0 +1,191 @@
+// The sum of a token's rows and its gradients:
+//   out[t] = sum_j w[t, j] y[slots[t, j]]
+//   d_y[slots[t, j]] = w[t, j] d_out[t],  d_w[t, j] = <d_out[t], y[slots[t, j]]>
+// with sums in FP32, j ascending, rounded once. A slot outside [0, R) names no
+// row and adds nothing. Without weights (w = 1) the sum is the gradient of a
+// permutation, and d_y a permutation itself.
+//
+// Both go by tokens: a token's row of d_out is read once for its topk rows, and
+// no two tokens meet in a row (a routing's slots are distinct), so nothing is
+// added in memory. HBM bounds the large calls, the chain slot -> row -> sum the
+// small.
+#include "moe_rows.h"
+#include "moe_step.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRowsAhead = 8;   // rows whose loads are in flight together
+
+// A thread sums 8 columns of a token. 1 << lg threads (a power of two, at most
+// 256) lie along a row, nb times where the row is longer.
+template <int TYPE>
+__global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type, int lg, int nb) {
+  const int blk = blockIdx.x / nb, cb = blockIdx.x - blk * nb;
+  const int64_t t = (int64_t)blk * (256 >> lg) + (threadIdx.x >> lg);
+  const int col = 8 * (cb * 256 + (threadIdx.x & ((1 << lg) - 1)));
+  if (t >= p.T || col >= p.H) return;
+  float acc[8] = {};
+  const int32_t* slots = p.slots + t * p.topk;
+  for (int j0 = 0; j0 < p.topk; j0 += kRowsAhead) {
+    int slot[kRowsAhead];
+    float w[kRowsAhead];
+    Raw8<TYPE> raw[kRowsAhead];
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      const bool in = j0 + j < p.topk;
+      slot[j] = in ? slots[j0 + j] : -1;
+      w[j] = in && p.w ? p.w[t * p.topk + j0 + j] : 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      raw[j].zero();
+      if (slot[j] >= 0 && slot[j] < p.R) raw[j].load(p.y, slot[j] * p.y_ld + col);
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      if (slot[j] < 0 || slot[j] >= p.R) continue;
+      float v[8];
+      raw[j].get(v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(w[j], v[k], acc[k]);
+    }
+  }
+  const int64_t at = t * p.out_ld + col;
+  if (out_type == TYPE_BF16) store8<TYPE_BF16>(p.out, at, acc);
+  else if (out_type == TYPE_F16) store8<TYPE_F16>(p.out, at, acc);
+  else store8<TYPE_F32>(p.out, at, acc);
+}
+
+constexpr int kHeld = 4;        // pieces of 8 values of d_out that a thread holds
+
+// TEAM threads (64 or 256) take `each` of a token's rows. Workgroups behind
+// those of the tokens look through 64 rows each for such as no token names and
+// write 0 there.
+template <int TYPE, int TEAM>
+__global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, int each, int teams_blocks) {
+  __shared__ float sums[4][64];   // of a wave, per row
+  __shared__ int pad[64];
+  __shared__ int pads;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if ((int)blockIdx.x >= teams_blocks) {
+    const int lo = p.offsets ? max(p.offsets[0], 0) : 0, hi = p.offsets ? min(p.offsets[p.E], p.R) : p.R;
+    const int r0 = ((int)blockIdx.x - teams_blocks) * 64;
+    if (threadIdx.x < 64) {
+      const int r = r0 + lane;
+      bool none = false;
+      if (r >= lo && r < hi) {
+        const int src = p.row_src[r];
+        none = src < 0 || (int64_t)src >= (int64_t)p.T * p.topk;
+      }
+      const uint64_t m = __ballot(none);
+      if (none) pad[__popcll(m & ((1ull << lane) - 1))] = r;
+      if (lane == 0) pads = __popcll(m);
+    }
+    __syncthreads();
+    const float zero[8] = {};
+    for (int i = wave; i < pads; i += 4)
+      for (int c = 8 * lane; c < p.H; c += 512) store8<TYPE>(p.d_y, pad[i] * p.dy_ld + c, zero);
+    return;
+  }
+  const int team = TEAM == 64 ? blockIdx.x * 4 + wave : blockIdx.x;
+  const int64_t t = team / parts;
+  const int id = TEAM == 64 ? lane : threadIdx.x;
+  if (t < p.T) {
+    const int j0 = (team - (int)t * parts) * each, j1 = min(j0 + each, p.topk);
+    float mine = 0.f;             // lane j: of row j0 + j, in this wave's columns
+    for (int base = 0; base < p.H; base += TEAM * 8 * kHeld) {
+      float d[kHeld][8];
+      int cols[kHeld];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        cols[i] = base + 8 * (i * TEAM + id);
+        Raw8<TYPE> raw;
+        raw.zero();
+        if (cols[i] < p.H) raw.load(p.d_out, t * p.d_ld + cols[i]);
+        raw.get(d[i]);
+      }
+      for (int j = j0; j < j1; ++j) {
+        const int slot = p.slots[t * p.topk + j];
+        if (slot < 0 || slot >= p.R) continue;
+        const float w = p.w ? p.w[t * p.topk + j] : 1.f;
+        float dot = 0.f;
+        if (p.y) {
+          Raw8<TYPE> raw[kHeld];
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) {
+            raw[i].zero();
+            if (cols[i] < p.H) raw[i].load(p.y, slot * p.y_ld + cols[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) {
+            float v[8];
+            raw[i].get(v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dot = __builtin_fmaf(d[i][k], v[k], dot);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          if (cols[i] >= p.H) continue;
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = w * d[i][k];
+          store8<TYPE>(p.d_y, slot * p.dy_ld + cols[i], v);
+        }
+        if (p.y) {
+          const float sum = wave_sum_of(dot);
+          if (lane == j - j0) mine += sum;
+        }
+      }
+    }
+    if (TEAM == 64) {
+      if (p.d_w && lane < j1 - j0) p.d_w[t * p.topk + j0 + lane] = mine;
+    } else {
+      sums[wave][lane] = mine;
+    }
+  }
+  if (TEAM == 256) {              // t < T for all of the workgroup, or for none
+    __syncthreads();
+    const int j0 = (team - (int)t * parts) * each, j1 = min(j0 + each, p.topk);
+    if (t < p.T && p.d_w && threadIdx.x < (unsigned)(j1 - j0))
+      p.d_w[t * p.topk + j0 + threadIdx.x] =
+          sums[0][threadIdx.x] + sums[1][threadIdx.x] + sums[2][threadIdx.x] + sums[3][threadIdx.x];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hipStream_t s) {
+  const int H8 = p.H / 8;
+  int lg = 0;
+  while (lg < 8 && (1 << lg) < H8) ++lg;
+  const int nb = (H8 + 255) / 256;
+  const int64_t g = ((int64_t)p.T + (256 >> lg) - 1) / (256 >> lg) * nb;
+  if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (type == TYPE_BF16) combine_sum<TYPE_BF16><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, nb);
+  else if (type == TYPE_F16) combine_sum<TYPE_F16><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, nb);
+  else combine_sum<TYPE_F32><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, nb);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_grad(const CombineParams& p, int type, hipStream_t s) {
+  const bool wide = p.H > 1024;
+  // few tokens: their rows one by one
+  const int parts = p.T >= 1024 ? 1 : p.topk, each = p.T >= 1024 ? p.topk : 1;
+  const int64_t teams = (int64_t)p.T * parts, blocks = wide ? teams : (teams + 3) / 4;
+  const int64_t g = blocks + (p.row_src ? (p.R + 63) / 64 : 0);
+  if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (g == 0) return hipSuccess;
+  auto go = [&](auto ty) {
+    constexpr int TYPE = decltype(ty)::value;
+    if (wide) combine_grad<TYPE, 256><<<(unsigned)g, 256, 0, s>>>(p, parts, each, (int)blocks);
+    else combine_grad<TYPE, 64><<<(unsigned)g, 256, 0, s>>>(p, parts, each, (int)blocks);
+  };
+  if (type == TYPE_BF16) go(std::integral_constant<int, TYPE_BF16>{});
+  else if (type == TYPE_F16) go(std::integral_constant<int, TYPE_F16>{});
+  else go(std::integral_constant<int, TYPE_F32>{});
+  return hipGetLastError();
+}
+
+}  // namespace moe
