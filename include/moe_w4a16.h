@@ -518,6 +518,36 @@ moe_status_t moe_mx_grouped_gemm(const uint8_t* aq, const uint8_t* a_scales, con
                                  int32_t M, int32_t N, int32_t K, void* out, int64_t out_ld,
                                  int32_t out_dtype, moe_stream_t stream);
 
+enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 };
+
+/* moe_grouped_gemm with an epilogue on its FP32 sums, rounded once:
+ *   out[r] = [residual[r] +] act(a[r] . w[e]^T [+ bias[e]])
+ * act NONE: the value, N columns; SWIGLU: w[e] is gate | up, its rows [0, N/2)
+ * and [N/2, N), and out has N/2 columns silu(gate) * up (N a multiple of 16).
+ *   bias      device [E, N] of bias_dtype (BF16, FP16 or FP32), rows bias_ld
+ *             values apart, or NULL
+ *   residual  device [M, columns of out] of out_dtype, rows res_ld values
+ *             apart, or NULL; may be `out` itself
+ * The residual's gradient is that of out; those of a, w and the bias are
+ * moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad and moe_grouped_bias_grad for
+ * the gradient before act (moe_swiglu_grad). Otherwise as moe_grouped_gemm. */
+moe_status_t moe_grouped_linear(const void* a, int64_t a_ld, const void* w, int64_t w_stride,
+                                int64_t w_ld, int32_t dtype, const int32_t* offsets, int32_t E,
+                                int32_t M, int32_t N, int32_t K, const void* bias,
+                                int32_t bias_dtype, int64_t bias_ld, int32_t act,
+                                const void* residual, int64_t res_ld, void* out, int64_t out_ld,
+                                int32_t out_dtype, moe_stream_t stream);
+
+/* Gradient of the biases: db[e] = sum over the rows r of e of dy[r]; 0 for an
+ * expert without rows.
+ *   dy   device [M, N] of dtype (BF16 or FP16), db device [E, N] of out_dtype,
+ *        rows db_ld values apart, fully written
+ * Otherwise as moe_grouped_gemm. */
+moe_status_t moe_grouped_bias_grad(const void* dy, int64_t dy_ld, int32_t dtype,
+                                   const int32_t* offsets, int32_t E, int32_t M, int32_t N,
+                                   void* db, int64_t db_ld, int32_t out_dtype,
+                                   moe_stream_t stream);
+
 /* ---- operators of a training step -------------------------------------------
  *
  * What lies between the router, the experts' products and their gradients.

@@ -159,3 +159,32 @@ def swiglu_grad(h, d_a):
     slack = torch.cat([(d * u).abs() * s * rel * (2 + 2 * g.abs()), du.abs() * rel], 1)
     lost = 2.0 ** -126 * (g < -87) * (1 + g.abs())       # of s, as in swiglu_slack
     return torch.cat([dg, du], 1), slack + torch.cat([(d * u).abs() * lost, d.abs() * lost], 1) + 2.0 ** -126
+
+
+# ---- product with an epilogue --------------------------------------------------------
+
+
+def linear(a, w, counts, bias, act, residual, start=0):
+    """(out, FP32's error before the last rounding) for the rows of the groups; 0 elsewhere."""
+    from tests.ops_util import groups
+    K, N = a.shape[1], w.shape[1]
+    half = N // 2
+    out = torch.zeros(a.shape[0], half if act == "swiglu" else N, dtype=torch.float64)
+    slack = torch.zeros_like(out)
+    for e, lo, hi in groups(counts, start):
+        x, v = a[lo:hi].double(), w[e].double()
+        b = torch.zeros(N, dtype=torch.float64) if bias is None else bias[e].double()
+        z = x @ v.T + b
+        err = (x.abs() @ v.abs().T) * (K + 1) * 2.0 ** -23 + z.abs() * 2.0 ** -24     # of the sum, of adding the bias
+        if act == "swiglu":
+            g, u, eg, eu = z[:, :half], z[:, half:], err[:, :half], err[:, half:]
+            s = torch.sigmoid(g)
+            z = g * s * u
+            # |d silu / dg| <= 1.1; s(g) within (2 |g| + 10) steps; lost where 1 / (1 + e^-g) is subnormal
+            err = 1.1 * eg * (u.abs() + eu) + (g * s).abs() * eu + z.abs() * (2 * g.abs() + 10) * 2.0 ** -23
+            err = err + 2.0 ** -126 * (1 + (g * u).abs() * (g < -87))
+        if residual is not None:
+            z = z + residual[lo:hi].double()
+            err = err + (z.abs() + err) * 2.0 ** -24
+        out[lo:hi], slack[lo:hi] = z, err
+    return out, slack

@@ -39,6 +39,8 @@ NOALLOC_SCRATCH_BYTES = 128 << 20
 MOE_SCALE_BF16 = 1
 MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
+ACTS = {"none": MOE_ACT_NONE, "swiglu": MOE_ACT_SWIGLU}
 SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 MOE_PACK_INT32_LOW_NIBBLE_FIRST_K = 1
 
@@ -53,6 +55,7 @@ EXPORTS = [
     "moe_profile_enable", "moe_profile_reset", "moe_profile_read",
     "moe_router_balance_bytes", "moe_router_balance", "moe_router_balance_grad", "moe_combine", "moe_combine_grad",
     "moe_mx8_scale_cols", "moe_mx8_quant", "moe_mx8_dequant", "moe_swiglu_save", "moe_swiglu_grad",
+    "moe_grouped_linear", "moe_grouped_bias_grad",
 ]
 
 
@@ -147,6 +150,9 @@ def lib() -> ctypes.CDLL:
         "moe_mx8_quant": (S, [P, I32, I64, I64, I32, P, P, P]),
         "moe_mx8_dequant": (S, [P, P, I64, I32, P, I32, P, I32, P, I32, I64, I64, P]),
         "moe_swiglu_save": (S, [P, I32, I64, I32, I32, P, I32, P, I64, P, P, P]),
+        "moe_grouped_linear": (S, [P, I64, P, I64, I64, I32, P, I32, I32, I32, I32, P, I32, I64, I32, P, I64, P, I64, I32,
+                                   P]),
+        "moe_grouped_bias_grad": (S, [P, I64, I32, P, I32, I32, I32, P, I64, I32, P]),
         "moe_swiglu_grad": (S, [P, I64, P, P, I32, I32, I32, P, I64, P, I32, P, I64, P, I64, P]),
         "moe_profile_enable": (S, [S]),
         "moe_profile_reset": (None, []),
@@ -618,6 +624,69 @@ def grouped_gemm_wgrad(dy, a, offsets, out=None, out_dtype=None, stream=None):
     _call((_lib or lib()).moe_grouped_gemm_wgrad, dev, stream,
           dy.data_ptr(), y_ld, a.data_ptr(), a_ld, _dtype(dy.dtype), offsets.data_ptr(), E, M, N, K,
           out.data_ptr(), stride, o_ld, _dtype(out.dtype))
+    return out
+
+
+def grouped_linear(a, w, offsets, bias=None, act="none", residual=None, out=None, out_dtype=None, stream=None):
+    """grouped_gemm with an epilogue on its FP32 sums, rounded once: out[r] =
+    [residual[r] +] act(a[r] . w[e]^T [+ bias[e]]). act "none", or "swiglu" for
+    w[e] = gate | up (N a multiple of 16): silu(gate) * up, [M, N/2].
+
+    bias [E, N] bf16, fp16 or fp32; residual of out's shape and dtype, may be
+    `out` itself. Gradients: grouped_gemm_dgrad, grouped_gemm_wgrad and
+    grouped_bias_grad for the gradient before act (swiglu_grad)."""
+    if _torch is None:
+        _load()
+    _need(a.dim() == 2 and w.dim() == 3, "a: [M, K], w: [E, N, K]")
+    M, K = a.shape
+    E, N, Kw = w.shape
+    if K != Kw:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"a has {K} columns, w {Kw}")
+    code = ACTS.get(act)
+    if code is None:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"act {act!r}: none or swiglu")
+    _fits(M | N | K | E)
+    dev = a.device
+    a_ld = _matrix(a, "a")
+    w_ld, w_stride = _weights(w, a.dtype, dev)
+    _dense(offsets, "offsets", _torch.int32, dev, (E + 1,))
+    cols = N // 2 if code else N
+    if out is None:
+        out = _new((M, cols), out_dtype or a.dtype, dev, stream)
+        o_ld = cols
+    else:
+        o_ld = _matrix(out, "out", out_dtype, dev, (M, cols))
+    b_at, b_type, b_ld = None, 0, 0
+    if bias is not None:
+        b_at, b_type, b_ld = bias.data_ptr(), _dtype(bias.dtype), _matrix(bias, "bias", None, dev, (E, N))
+    r_ld = 0 if residual is None else _matrix(residual, "residual", out.dtype, dev, (M, cols))
+    _call((_lib or lib()).moe_grouped_linear, dev, stream,
+          a.data_ptr(), a_ld, w.data_ptr(), w_stride, w_ld, _dtype(a.dtype), offsets.data_ptr(), E, M, N, K,
+          b_at, b_type, b_ld, code, None if residual is None else residual.data_ptr(), r_ld,
+          out.data_ptr(), o_ld, _dtype(out.dtype))
+    return out
+
+
+def grouped_bias_grad(dy, offsets, out=None, out_dtype=None, stream=None):
+    """Gradient of grouped_linear's bias: out[e] = the sum of dy's rows of e,
+    [E, N] of out_dtype (default dy's; fp32 as well); 0 for an expert without
+    rows. dy [M, N] bf16 or fp16, N a multiple of 8."""
+    if _torch is None:
+        _load()
+    _need(dy.dim() == 2, "dy: [M, N]")
+    M, N = dy.shape
+    dev = dy.device
+    y_ld = _matrix(dy, "dy")
+    _need(offsets is not None, "offsets: [E + 1]")
+    off, E = _offsets(offsets, dev)
+    _fits(M | N | E)
+    if out is None:
+        out = _new((E, N), out_dtype or dy.dtype, dev, stream)
+        o_ld = N
+    else:
+        o_ld = _matrix(out, "out", out_dtype, dev, (E, N))
+    _call((_lib or lib()).moe_grouped_bias_grad, dev, stream,
+          dy.data_ptr(), y_ld, _dtype(dy.dtype), off, E, M, N, out.data_ptr(), o_ld, _dtype(out.dtype))
     return out
 
 

@@ -18,6 +18,17 @@ namespace moe {
 enum RaggedWay : int { WAY_FWD = 0, WAY_DGRAD = 1, WAY_WGRAD = 2, WAY_MX = 3 };
 enum RaggedType : int { TYPE_BF16 = 0, TYPE_F16 = 1, TYPE_F32 = 2 };   // moe_dtype_t
 
+// What a forward product does with its sums before they are rounded: with
+// swiglu the weights' rows are gate | up, and the output silu(gate) * up.
+struct Epilogue {
+  const void* bias;         // [E][bias_ld] or NULL
+  int64_t bias_ld;
+  int bias_type;
+  int swiglu;
+  const void* res;          // [M][res_ld] of the output's type, or NULL
+  int64_t res_ld;
+};
+
 struct RaggedParams {
   const void* p;          // weights (wgrad: a)
   const void* q;          // token rows (a; dgrad and wgrad: dy)
@@ -34,10 +45,14 @@ struct RaggedParams {
   int64_t out_ld, out_stride;    // elements; wgrad: from expert to expert
   int out_type;
   int stream_out;         // set by the launcher: the output passes the caches by
+  Epilogue epi;           // launch_ragged_linear (I: columns of the output, half the weights' rows with swiglu)
 };
 
 // type: of both operands (bf16 / f16), ignored for WAY_MX.
 hipError_t launch_ragged_gemm(const RaggedParams& p, int way, int type, hipStream_t s);
+
+// The forward product with p.epi.
+hipError_t launch_ragged_linear(const RaggedParams& p, int type, hipStream_t s);
 
 // e2m1 codes (low nibble first) and E8M0 scale bytes of `rows` rows of K
 // values, and back. x_ld / out_ld in elements; codes [rows][K/2], scales

@@ -100,16 +100,7 @@ struct SwigluParams {
 hipError_t launch_swiglu_save(const SwigluParams& p, int type, hipStream_t s);
 hipError_t launch_swiglu_grad(const SwigluParams& p, int type, hipStream_t s);
 
-// ---- the experts' product with an epilogue ----
-
-struct Epilogue {
-  const void* bias;         // [E][bias_ld] or NULL
-  int64_t bias_ld;
-  int bias_type;
-  int swiglu;
-  const void* res;          // [M][res_ld] of the output's type, or NULL
-  int64_t res_ld;
-};
+// ---- gradient of the experts' biases ----
 
 struct BiasGradParams {
   const void* dy;           // [M][ld]

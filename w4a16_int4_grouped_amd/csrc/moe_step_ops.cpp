@@ -1,10 +1,12 @@
 // C ABI of the operators of a training step around the experts' products:
 // balance loss of the router, a token's sum of rows, rows in 8 bits, SwiGLU
-// with such a checkpoint, and their gradients. Arguments are validated here
+// with such a checkpoint, and their gradients, and the experts' product with an
+// epilogue. Arguments are validated here
 // before anything is enqueued.
 #include <hip/hip_runtime.h>
 
 #include "moe_ops_check.h"
+#include "moe_ragged.h"
 #include "moe_step.h"
 
 using namespace moe;
@@ -237,6 +239,54 @@ moe_status_t moe_swiglu_grad(const void* h, int64_t h_ld, const int8_t* q, const
   p.q_in = q, p.scales_in = scales, p.d_a = d_a, p.da_ld = da_ld, p.d_h = d_h, p.dh_ld = dh_ld, p.a = a, p.a_ld = a_ld;
   const hipStream_t s = (hipStream_t)stream;
   return launched(run("swiglu_grad", s, [&] { return launch_swiglu_grad(p, dtype, s); }), "SwiGLU gradient launch");
+}
+
+moe_status_t moe_grouped_linear(const void* a, int64_t a_ld, const void* w, int64_t w_stride, int64_t w_ld,
+                                int32_t dtype, const int32_t* offsets, int32_t E, int32_t M, int32_t N, int32_t K,
+                                const void* bias, int32_t bias_dtype, int64_t bias_ld, int32_t act,
+                                const void* residual, int64_t res_ld, void* out, int64_t out_ld, int32_t out_dtype,
+                                moe_stream_t stream) {
+  moe_status_t st = check_groups(dtype, offsets, E, M, N, K, out_dtype, 8);
+  if (st != MOE_OK) return st;
+  if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return fail(MOE_ERR_INVALID_ARG, "act = %d", act);
+  const bool glu = act == MOE_ACT_SWIGLU;
+  if (glu && N % 16) return fail(MOE_ERR_INVALID_ARG, "N = %d: a multiple of 16 for gate | up weights", N);
+  if (bias) {
+    if (!type_ok(bias_dtype)) return fail(MOE_ERR_INVALID_ARG, "bias_dtype = %d", bias_dtype);
+    if ((st = check_matrix("bias", bias, bias_ld, N)) != MOE_OK) return st;
+  }
+  if (M == 0) return ok();
+  const int I = glu ? N / 2 : N;
+  if ((st = check_matrix("a", a, a_ld, K)) != MOE_OK || (st = check_matrix("w", w, w_ld, K)) != MOE_OK ||
+      (st = check_matrix("out", out, out_ld, I)) != MOE_OK ||
+      (residual && (st = check_matrix("residual", residual, res_ld, I)) != MOE_OK))
+    return st;
+  if (w_stride % 8 || w_stride < 0) return fail(MOE_ERR_INVALID_ARG, "w: experts not a multiple of 8 values apart");
+  RaggedParams p{};
+  p.p = w, p.p_stride = w_stride * 2, p.p_ld = w_ld * 2;
+  p.q = a, p.q_ld = a_ld * 2;
+  p.offsets = offsets, p.E = E, p.M = M, p.I = I, p.C = K;
+  p.out = out, p.out_ld = out_ld, p.out_type = out_dtype;
+  p.epi.bias = bias, p.epi.bias_ld = bias_ld, p.epi.bias_type = bias_dtype;
+  p.epi.swiglu = glu, p.epi.res = residual, p.epi.res_ld = res_ld;
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(run("grouped_linear", s, [&] { return launch_ragged_linear(p, dtype, s); }),
+                  "grouped linear launch");
+}
+
+moe_status_t moe_grouped_bias_grad(const void* dy, int64_t dy_ld, int32_t dtype, const int32_t* offsets, int32_t E,
+                                   int32_t M, int32_t N, void* db, int64_t db_ld, int32_t out_dtype,
+                                   moe_stream_t stream) {
+  moe_status_t st = check_groups(dtype, offsets, E, M, N, 8, out_dtype, 8);
+  if (st != MOE_OK) return st;
+  if ((M > 0 && (st = check_matrix("dy", dy, dy_ld, N)) != MOE_OK) ||
+      (st = check_matrix("db", db, db_ld, N)) != MOE_OK)
+    return st;
+  BiasGradParams p{};
+  p.dy = dy, p.ld = dy_ld, p.offsets = offsets, p.E = E, p.M = M, p.N = N, p.db = db, p.db_ld = db_ld;
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(run("grouped_bias_grad", s, [&] { return launch_bias_grad(p, dtype, out_dtype, s); }),
+                  "bias gradient launch");
 }
 
 }  // extern "C"
