@@ -62,14 +62,19 @@ __device__ __forceinline__ Rows sequence(const BalanceParams& p, int s) {
   return Rows{lo, max(min(p.offsets[s + 1], p.T), lo)};
 }
 
-// The first sequence that ends behind row r, S if none does.
+// The first sequence that ends behind row r, S if none does, for a whole wave:
+// its lanes look at 64 of them at a time.
 __device__ __forceinline__ int sequence_at(const BalanceParams& p, int r) {
   if (!p.offsets) return 0;
-  int a = 0, b = p.S;
-  while (a < b) {
-    const int m = (a + b) / 2;
-    if (p.offsets[m + 1] > r) b = m;
-    else a = m + 1;
+  const int lane = threadIdx.x & 63;
+  int a = 0, n = p.S;                    // it is one of a .. a + n
+  while (n > 0) {
+    const int step = (n + 63) / 64, at = min((lane + 1) * step, n) - 1;
+    const uint64_t past = __ballot(p.offsets[a + at + 1] > r);
+    if (!past) return a + n;
+    const int f = __builtin_ctzll(past);
+    a += f * step;
+    n = step == 1 ? 0 : min(step, n - f * step) - 1;   // (the last of them is one that does)
   }
   return a;
 }
@@ -80,69 +85,95 @@ __device__ __forceinline__ int expert_of(int lane, int place) {
   return V * lane + 64 * V * (place / V) + place % V;
 }
 
-template <int TYPE, int VPL, int V>
-__device__ __forceinline__ void load_row(const void* x, int64_t row, int E, int lane, float (&l)[VPL], float none) {
+// A row as loaded: the conversions stand behind the loads, so that those of
+// several rows are in flight together. Places without an expert, and rows
+// without `has`, hold -inf, or with ZERO 0.
+template <int TYPE, int VPL, int V, bool ZERO = false>
+struct RowRaw {
+  static constexpr bool F32 = TYPE == TYPE_F32;
+  static constexpr uint32_t kNone = ZERO ? 0u : F32 ? 0xFF800000u : TYPE == TYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  static constexpr int kWords = F32 ? VPL : (VPL + 1) / 2;
+  uint32_t w[V == 1 ? VPL : kWords];
+  __device__ __forceinline__ void load(const void* x, int64_t row, int E, int lane, bool has) {
 #pragma unroll
-  for (int g = 0; g < VPL; g += V) {
-    const int e = expert_of<V>(lane, g);
-#pragma unroll
-    for (int i = 0; i < V; ++i) l[g + i] = none;
-    if (e >= E) continue;
-    if constexpr (V == 1) {
-      l[g] = load1<TYPE>(x, row + e);
-    } else if constexpr (TYPE == TYPE_F32) {
-      const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(x) + row + e);
-      l[g] = v.x, l[g + 1] = v.y;
-    } else {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(x) + row + e);
-      if constexpr (TYPE == TYPE_BF16) {
-        l[g] = bf16_lo(v), l[g + 1] = bf16_hi(v);
+    for (int g = 0; g < VPL; g += V) {
+      const int e = expert_of<V>(lane, g);
+      const bool in = has && e < E;
+      if constexpr (V == 1) {
+        w[g] = kNone;
+        if (in) {
+          if constexpr (F32) w[g] = static_cast<const uint32_t*>(x)[row + e];
+          else w[g] = static_cast<const uint16_t*>(x)[row + e];
+        }
+      } else if constexpr (F32) {
+        u32x2_t v = {kNone, kNone};
+        if (in) v = *reinterpret_cast<const u32x2_t*>(static_cast<const float*>(x) + row + e);
+        w[g] = v[0], w[g + 1] = v[1];
       } else {
-        const f16x2_t h = __builtin_bit_cast(f16x2_t, v);
-        l[g] = (float)h[0], l[g + 1] = (float)h[1];
+        w[g / 2] = kNone;
+        if (in) w[g / 2] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(x) + row + e);
       }
     }
   }
-}
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (F32) return __uint_as_float(w[i]);
+    const uint32_t h = V == 1 ? w[i] : i & 1 ? w[i / 2] >> 16 : w[i / 2];
+    if constexpr (TYPE == TYPE_BF16) return __uint_as_float(h << 16);
+    else return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+  }
+};
+
+// e^x by v_exp_f32: x log2 e rounded moves it by up to |x| 2^-24 of itself, and
+// results below 2^-126 are 0.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // l becomes the scores, `rest` what remains of 1 above the sigmoid (softmax: 1).
-// Where every sigmoid is below e^-60 they are e^l to FP32 accuracy, and e^(l -
-// top) does not vanish.
+// Where the sigmoids' sum would lose them to FP32's small end, they are e^l to
+// FP32 accuracy, and e^(l - top) does not vanish.
 template <int VPL>
 __device__ __forceinline__ void scores(float (&l)[VPL], int sigmoid_scores, float (&rest)[VPL]) {
-  float top = -INFINITY;
+  float v[VPL], total = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) l[i] = clean(l[i]), top = fmaxf(top, l[i]);
-  top = wave_max_of(top);
-  if (top == -INFINITY) top = 0.f;
-  float total = 0.f;
-  if (sigmoid_scores && top > -60.f) {
+  for (int i = 0; i < VPL; ++i) l[i] = l[i] >= -kMax ? fminf(l[i], kMax) : -INFINITY, rest[i] = 1.f;
+  if (sigmoid_scores) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const float x = expf(-fabsf(l[i])), y = 1.0f / (1.0f + x);   // sigmoid(|l|) = y, sigmoid(-|l|) = x y
-      const float xy = l[i] == -INFINITY ? 0.f : x * y;
+      const float x = exp_of(-fabsf(l[i])), y = __builtin_amdgcn_rcpf(1.0f + x);   // sigmoid(|l|) = y, sigmoid(-|l|) = x y
+      const float xy = x * y;
+      v[i] = l[i] < 0.f ? xy : y;
       rest[i] = l[i] < 0.f ? y : xy;
-      l[i] = l[i] < 0.f ? xy : y;
-      total += l[i];
+      total += v[i];
     }
-  } else {
+    total = wave_sum_of(total);
+  }
+  if (!sigmoid_scores || total < 0x1p-80f) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) top = fmaxf(top, l[i]);
+    top = wave_max_of(top);
+    if (top == -INFINITY) top = 0.f;
+    total = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      l[i] = expf(l[i] - top);
+      v[i] = exp_of(l[i] - top);
       rest[i] = 1.f;
-      total += l[i];
+      total += v[i];
     }
+    total = wave_sum_of(total);
   }
-  total = wave_sum_of(total);
-  const float inv = total > 0.f ? 1.0f / total : 0.f;
+  const float inv = total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) l[i] *= inv;
+  for (int i = 0; i < VPL; ++i) l[i] = v[i] * inv;
 }
+
+// Rows of a wave whose loads are in flight together.
+constexpr int rows_ahead(int VPL) { return VPL <= 8 ? 4 : VPL <= 16 ? 2 : 1; }
 
 // W waves sum a chunk. SOLO: the one chunk of the one sequence: counts and loss at once.
 template <int TYPE, int VPL, int V, int W, bool SOLO>
 __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceWs ws) {
-  constexpr int kE = 64 * VPL;
+  constexpr int kE = 64 * VPL, NR = rows_ahead(VPL);
   __shared__ float part[W][kE];
   __shared__ int hist[kE];
   __shared__ double shares[W];
@@ -153,6 +184,14 @@ __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceW
     int* ticket = reinterpret_cast<int*>(base + ws.ticket_at);
     for (int s = threadIdx.x; s < p.S; s += 64 * W) ticket[s] = 0;
   }
+  // the first rows and ids of the chunk, whatever sequence they belong to
+  RowRaw<TYPE, VPL, V> raw[NR];
+  const int mine = r0 + wave * NR;
+  int held = mine;             // the row that raw begins with
+#pragma unroll
+  for (int n = 0; n < NR; ++n) raw[n].load(p.logits, (int64_t)(mine + n) * p.ld, p.E, lane, mine + n < r1);
+  const int64_t id_first = (int64_t)r0 * p.topk + threadIdx.x, id_end = (int64_t)r1 * p.topk;
+  const int first_id = id_first < id_end ? p.ids[id_first] : -1;
   for (int s = SOLO ? 0 : sequence_at(p, r0); s < p.S; ++s) {
     Rows q = sequence(p, s);
     if (!SOLO && q.lo >= r1) break;
@@ -161,16 +200,28 @@ __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceW
     for (int e = threadIdx.x; e < kE; e += 64 * W) hist[e] = 0;
     __syncthreads();
     float sum[VPL] = {};
-    for (int r = q.lo + wave; r < q.hi; r += W) {
-      float l[VPL], rest[VPL];
-      load_row<TYPE, VPL, V>(p.logits, (int64_t)r * p.ld, p.E, lane, l, -INFINITY);
-      scores(l, p.sigmoid, rest);
+    for (int r = mine; r < q.hi; r += W * NR) {
+      if (r + NR <= q.lo) continue;
+      if (r != held) {
+        held = r;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum[i] += l[i];
+        for (int n = 0; n < NR; ++n) raw[n].load(p.logits, (int64_t)(r + n) * p.ld, p.E, lane, r + n < r1);
+      }
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        if (r + n < q.lo || r + n >= q.hi) continue;
+        float l[VPL], rest[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = raw[n].get(i);
+        scores(l, p.sigmoid, rest);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sum[i] += l[i];
+      }
     }
-    const int64_t end = (int64_t)q.hi * p.topk;
-    for (int64_t i = (int64_t)q.lo * p.topk + threadIdx.x; i < end; i += 64 * W) {
-      const int e = p.ids[i];
+    const int64_t id_lo = (int64_t)q.lo * p.topk, id_hi = (int64_t)q.hi * p.topk;
+    for (int64_t i = id_first; i < id_hi; i += 64 * W) {
+      if (i < id_lo) continue;
+      const int e = i == id_first ? first_id : p.ids[i];
       if (e >= 0 && e < p.E) atomicAdd(&hist[e], 1);
     }
 #pragma unroll
@@ -258,34 +309,43 @@ __global__ __launch_bounds__(64 * kFinishWaves) void balance_finish(BalanceParam
   if (lane == 0) p.loss[s] = (float)(share * scale);
 }
 
-constexpr int kGradRows = 4;   // rows of a wave, one after another
-
 template <int TYPE, int VPL, int V>
 __global__ __launch_bounds__(256) void balance_grad(BalanceParams p) {
+  constexpr int NR = rows_ahead(VPL);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * kGradRows;
-  const int r0 = (int)first, r1 = (int)min(first + kGradRows, (int64_t)p.T);
+  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * NR;
   if (first >= p.T) return;
+  const int r0 = (int)first;
+  RowRaw<TYPE, VPL, V> raw[NR];
+  RowRaw<TYPE, VPL, V, true> add[NR];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    raw[n].load(p.logits, (first + n) * p.ld, p.E, lane, first + n < p.T);
+    if (p.add) add[n].load(p.add, (first + n) * p.add_ld, p.E, lane, first + n < p.T);
+  }
   int s = sequence_at(p, r0), has = -1;   // the row's sequence, and whose coefficients c holds
   Rows q = s < p.S ? sequence(p, s) : Rows{0, 0};
-  float c[VPL];
-  for (int r = r0; r < r1; ++r) {
+  float c[VPL] = {};
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const int r = r0 + n;
+    if (r >= p.T) return;
     while (s < p.S && r >= q.hi)
       if (++s < p.S) q = sequence(p, s);
-    if (s < p.S && s != has) {
-      const double n = q.hi - q.lo;
-      const float scale = n > 0 ? (float)((double)p.d_loss[s] * p.E / (n * n * p.topk)) : 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = expert_of<V>(lane, i);
-        c[i] = e < p.E ? scale * (float)p.counts_in[(int64_t)s * p.E + e] : 0.f;
-      }
-      has = s;
-    }
-    float l[VPL], rest[VPL], add[VPL];
-    if (p.add) load_row<TYPE, VPL, V>(p.add, (int64_t)r * p.add_ld, p.E, lane, add, 0.f);
+    float l[VPL], rest[VPL];
     if (s < p.S && r >= q.lo) {
-      load_row<TYPE, VPL, V>(p.logits, (int64_t)r * p.ld, p.E, lane, l, -INFINITY);
+      if (s != has) {
+        const double rows = q.hi - q.lo;
+        const float scale = (float)((double)p.d_loss[s] * p.E / (rows * rows * p.topk));
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const int e = expert_of<V>(lane, i);
+          c[i] = e < p.E ? scale * (float)p.counts_in[(int64_t)s * p.E + e] : 0.f;
+        }
+        has = s;
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = raw[n].get(i);
       scores(l, p.sigmoid, rest);
       float dot = 0.f;
 #pragma unroll
@@ -299,7 +359,7 @@ __global__ __launch_bounds__(256) void balance_grad(BalanceParams p) {
     }
     if (p.add) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) l[i] += add[i];
+      for (int i = 0; i < VPL; ++i) l[i] += add[n].get(i);
     }
     const int64_t row = (int64_t)r * p.d_ld;
 #pragma unroll
@@ -384,9 +444,10 @@ hipError_t launch_balance(const BalanceParams& p, int type, hipStream_t s) {
 
 hipError_t launch_balance_grad(const BalanceParams& p, int type, hipStream_t s) {
   const bool two = pairs(p.logits, p.ld, type) && pairs(p.add, p.add_ld, type) && pairs(p.d_logits, p.d_ld, type);
-  const unsigned n = (unsigned)((p.T + 4 * kGradRows - 1) / (4 * kGradRows));
   return by_type(type, [&](auto ty) {
     return by_experts(p.E, two, [&](auto vpl, auto v) {
+      constexpr int rows = 4 * rows_ahead(decltype(vpl)::value);
+      const unsigned n = (unsigned)((p.T + rows - 1) / rows);
       balance_grad<decltype(ty)::value, decltype(vpl)::value, decltype(v)::value><<<n, 256, 0, s>>>(p);
       return hipGetLastError();
     });

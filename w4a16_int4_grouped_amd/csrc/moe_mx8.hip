@@ -27,13 +27,46 @@ __device__ __forceinline__ Range live_rows(const LiveRows& l, int64_t rows) {
   return Range{lo, max(min((int64_t)l.offsets[l.E], rows), lo)};
 }
 
-// Group i among rows of n: by 32-bit division where the call's groups allow it.
-__device__ __forceinline__ Place group_place(int64_t i, int n, bool small) {
-  if (small) {
-    const uint32_t r = (uint32_t)i / (uint32_t)n;
-    return Place{(int64_t)r, (int)((uint32_t)i - r * (uint32_t)n)};
+// A workgroup's threads along rows of n groups of 8 values, `each` groups a
+// thread. One division at most, and the same row for a wave's lanes wherever a
+// row has more than 32 groups, so that rows, their sources and addresses are
+// scalars.
+//   NARROW  up to 32 groups: 1 << lg threads on a row (a power of two)
+//   ROWS    up to 256 groups: the same, at least a wave on a row
+//   WIDE    longer rows: a workgroup on 256 * each groups of one row
+enum Mode : int { NARROW = 0, ROWS = 1, WIDE = 2 };
+
+struct Shape {
+  int mode, lg, chunks;   // WIDE: chunks of a row
+  unsigned blocks;        // workgroups, 0: too many for a grid
+};
+
+Shape shape_of(int64_t rows, int n, int each) {
+  Shape s{n > 256 ? WIDE : n > 32 ? ROWS : NARROW, 0, 1, 0};
+  while (s.lg < 8 && (1 << s.lg) < n) ++s.lg;
+  int64_t g;
+  if (s.mode == WIDE) {
+    s.chunks = (n + 256 * each - 1) / (256 * each);
+    g = rows * s.chunks;
+  } else {
+    const int64_t per = (int64_t)each * (256 >> s.lg);
+    g = (rows + per - 1) / per;
   }
-  return place_of(i, n);
+  s.blocks = g > 0x7FFFFFFF ? 0u : (unsigned)g;
+  return s;
+}
+
+// Row and group of a thread's b-th place.
+template <int MODE, int EACH>
+__device__ __forceinline__ Place place(const Shape& s, int b) {
+  const uint32_t blk = blockIdx.x;
+  const int tid = threadIdx.x;
+  if constexpr (MODE == WIDE) {
+    const uint32_t r = s.chunks == 1 ? blk : blk / (uint32_t)s.chunks;
+    return Place{(int64_t)r, (int)(blk - r * (uint32_t)s.chunks) * (256 * EACH) + 256 * b + tid};
+  }
+  const int row = MODE == ROWS ? __builtin_amdgcn_readfirstlane(tid >> s.lg) : tid >> s.lg;
+  return Place{((int64_t)blk * EACH + b) * (256 >> s.lg) + row, tid & ((1 << s.lg) - 1)};
 }
 
 // Scale byte of the quad's block, in its four lanes (255: not finite).
@@ -65,12 +98,15 @@ __device__ __forceinline__ u32x2_t encode(const float (&v)[8], uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ void decode(u32x2_t w, uint32_t b, float (&v)[8]) {
+// 2^(b - 133), which is subnormal below b = 7; NaN for 255.
+__device__ __forceinline__ float step_of(uint32_t b) {
+  return __uint_as_float(b == 255 ? 0x7FC00000u : b > 6 ? (b - 6) << 23 : 1u << (b + 16));
+}
+
+// Eight codes times s, exactly.
+__device__ __forceinline__ void decode(u32x2_t w, float s, float (&v)[8]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int q = (int)(w[k >> 2] << (24 - 8 * (k & 3))) >> 24;
-    v[k] = b == 255 ? __uint_as_float(0x7FC00000u) : __builtin_amdgcn_ldexpf((float)q, (int)b - 133);
-  }
+  for (int k = 0; k < 8; ++k) v[k] = (float)(int8_t)(w[k >> 2] >> (8 * (k & 3))) * s;
 }
 
 // Codes and scale of group c of a row of K8, and behind a row's last scale the
@@ -85,69 +121,78 @@ __device__ __forceinline__ void store_codes(int8_t* q, uint8_t* scales, int c, i
   }
 }
 
-constexpr int kBatch = 4;   // groups per thread
+constexpr int kQuant = 4, kDequant = 4, kPairs = 2;   // groups per thread (pairs: of both halves)
+constexpr int kRoutedRows = 4;                        // WIDE rows of a workgroup, where they are those of a routing
 
-template <int TYPE>
+template <int TYPE, int MODE>
 __global__ __launch_bounds__(256) void mx8_quant(const void* __restrict__ x, int64_t rows, int K8, int64_t ld,
                                                  int8_t* __restrict__ q, uint8_t* __restrict__ scales, int s_ld,
-                                                 bool small) {
-  const int n = (K8 + 3) & ~3;   // a row's lanes
-  const Place step{256 / n, 256 % n};
-  Place p = group_place((int64_t)blockIdx.x * (256 * kBatch) + threadIdx.x, n, small);
-  Raw8<TYPE> raw[kBatch];
-  Place at[kBatch];
+                                                 Shape sh) {
+  Raw8<TYPE> raw[kQuant];
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    at[b] = p;
+  for (int b = 0; b < kQuant; ++b) {
+    const Place p = place<MODE, kQuant>(sh, b);
     raw[b].zero();
     if (p.r < rows && p.c < K8) raw[b].load(x, p.r * ld + 8 * p.c);
-    advance(p, step, n);
   }
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
+  for (int b = 0; b < kQuant; ++b) {
+    const Place p = place<MODE, kQuant>(sh, b);
     float v[8];
     raw[b].get(v);
     const uint32_t sc = block_scale(v);
     const u32x2_t codes = encode(v, sc);
-    const int64_t r = at[b].r;
-    if (r < rows && at[b].c < K8) store_codes(q + r * 8 * K8, scales + r * s_ld, at[b].c, K8, s_ld, codes, sc);
+    if (p.r < rows && p.c < K8) store_codes(q + p.r * 8 * K8, scales + p.r * s_ld, p.c, K8, s_ld, codes, sc);
   }
 }
 
-template <int TYPE>
-__global__ __launch_bounds__(256) void mx8_dequant(Mx8Rows m, bool small) {
+// NR rows at a time (WIDE), so that the chain from a row's source to its codes
+// is waited for once for all of them.
+template <int TYPE, int MODE, int NR>
+__global__ __launch_bounds__(256) void mx8_dequant(Mx8Rows m, Shape sh) {
   const int K8 = m.K / 8;
   const Range live = live_rows(m.live, m.out_rows);
-  const Place step{256 / K8, 256 % K8};
-  const int64_t first = (int64_t)blockIdx.x * (256 * kBatch);
-  Place p = group_place(first + threadIdx.x, K8, small);
-  u32x2_t w[kBatch];
-  uint32_t e[kBatch];
-  Place at[kBatch];
+  int64_t src[NR][kDequant];
+  u32x2_t w[NR][kDequant];
+  uint32_t e[NR][kDequant];
+  auto at = [&](int n, int b) {
+    Place p = place<MODE, kDequant>(sh, b);
+    if (MODE == WIDE) p.r = p.r * NR + n;
+    return p;
+  };
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    at[b] = p;
-    int64_t r = p.r;
-    bool has = r >= live.lo && r < live.hi;
-    if (has && m.row_src) {
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int b = 0; b < kDequant; ++b) {
+      const int64_t r = at(n, b).r;
+      src[n][b] = -1;
+      if (r < live.lo || r >= live.hi) continue;
+      src[n][b] = r;
+      if (!m.row_src) continue;
       const int id = m.row_src[r];
-      r = (uint32_t)id / (uint32_t)m.topk;
-      has = id >= 0 && r < m.rows;
+      const uint32_t from = m.topk == 1 ? (uint32_t)id : (uint32_t)id / (uint32_t)m.topk;
+      src[n][b] = id >= 0 && from < m.rows ? (int64_t)from : -1;
     }
-    w[b] = u32x2_t{}, e[b] = 0;
-    if (has) {
-      w[b] = *reinterpret_cast<const u32x2_t*>(m.q + r * m.K + 8 * p.c);
-      e[b] = m.scales[r * m.s_ld + (p.c >> 2)];
-    }
-    advance(p, step, K8);
-  }
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    if (at[b].r < live.lo || at[b].r >= live.hi) continue;
-    float v[8];
-    decode(w[b], e[b], v);
-    store8<TYPE>(m.out, at[b].r * m.ld + 8 * at[b].c, v);
-  }
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int b = 0; b < kDequant; ++b) {
+      const int c = at(n, b).c;
+      w[n][b] = u32x2_t{}, e[n][b] = 0;
+      if (src[n][b] < 0 || c >= K8) continue;
+      w[n][b] = *reinterpret_cast<const u32x2_t*>(m.q + src[n][b] * m.K + 8 * c);
+      e[n][b] = m.scales[src[n][b] * m.s_ld + (c >> 2)];
+    }
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int b = 0; b < kDequant; ++b) {
+      const Place p = at(n, b);
+      if (p.r < live.lo || p.r >= live.hi || p.c >= K8) continue;
+      float v[8];
+      decode(w[n][b], step_of(e[n][b]), v);
+      store8<TYPE>(m.out, p.r * m.ld + 8 * p.c, v);
+    }
 }
 
 // sigmoid(g): for 16-bit rows by v_exp_f32 and v_rcp_f32, off by a few 2^-24
@@ -159,79 +204,67 @@ __device__ __forceinline__ float sigma(float g) {
   else return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
 }
 
-constexpr int kPairs = 2;   // groups per thread, of both halves
-
 // a = g s(g) u, and g | u in 8 bits, each half of a row in blocks of its own.
-template <int TYPE>
-__global__ __launch_bounds__(256) void swiglu_save(SwigluParams s, bool small) {
-  const int I8 = s.I / 8, n = (I8 + 3) & ~3;
+template <int TYPE, int MODE>
+__global__ __launch_bounds__(256) void swiglu_save(SwigluParams s, Shape sh) {
+  const int I8 = s.I / 8;
   const Range live = live_rows(s.live, s.rows);
-  const Place step{256 / n, 256 % n};
-  Place p = group_place((int64_t)blockIdx.x * (256 * kPairs) + threadIdx.x, n, small);
   Raw8<TYPE> rg[kPairs], ru[kPairs];
-  Place at[kPairs];
 #pragma unroll
   for (int b = 0; b < kPairs; ++b) {
-    at[b] = p;
+    const Place p = place<MODE, kPairs>(sh, b);
     rg[b].zero(), ru[b].zero();
     if (p.r >= live.lo && p.r < live.hi && p.c < I8) {
       rg[b].load(s.h, p.r * s.h_ld + 8 * p.c);
       ru[b].load(s.h, p.r * s.h_ld + s.I + 8 * p.c);
     }
-    advance(p, step, n);
   }
 #pragma unroll
   for (int b = 0; b < kPairs; ++b) {
+    const Place p = place<MODE, kPairs>(sh, b);
     float g[8], u[8], a[8];
     rg[b].get(g), ru[b].get(u);
     const uint32_t bg = block_scale(g), bu = block_scale(u);
     const u32x2_t cg = encode(g, bg), cu = encode(u, bu);
 #pragma unroll
     for (int k = 0; k < 8; ++k) a[k] = g[k] * sigma<TYPE>(g[k]) * u[k];
-    const int64_t r = at[b].r;
-    if (r < live.lo || r >= live.hi || at[b].c >= I8) continue;
-    store8<TYPE>(s.a, r * s.a_ld + 8 * at[b].c, a);
-    store_codes(s.q + 2 * r * s.I, s.scales + 2 * r * s.s_ld, at[b].c, I8, s.s_ld, cg, bg);
-    store_codes(s.q + (2 * r + 1) * s.I, s.scales + (2 * r + 1) * s.s_ld, at[b].c, I8, s.s_ld, cu, bu);
+    if (p.r < live.lo || p.r >= live.hi || p.c >= I8) continue;
+    store8<TYPE>(s.a, p.r * s.a_ld + 8 * p.c, a);
+    store_codes(s.q + 2 * p.r * s.I, s.scales + 2 * p.r * s.s_ld, p.c, I8, s.s_ld, cg, bg);
+    store_codes(s.q + (2 * p.r + 1) * s.I, s.scales + (2 * p.r + 1) * s.s_ld, p.c, I8, s.s_ld, cu, bu);
   }
 }
 
 // dg = da u s (1 + g (1 - s)), du = da g s, and a = g s u again.
-template <int TYPE, bool PACKED>
-__global__ __launch_bounds__(256) void swiglu_grad(SwigluParams s, bool small) {
+template <int TYPE, int MODE, bool PACKED>
+__global__ __launch_bounds__(256) void swiglu_grad(SwigluParams s, Shape sh) {
   const int I8 = s.I / 8;
   const Range live = live_rows(s.live, s.rows);
-  const Place step{256 / I8, 256 % I8};
-  Place p = group_place((int64_t)blockIdx.x * (256 * kPairs) + threadIdx.x, I8, small);
   Raw8<TYPE> rg[kPairs], ru[kPairs], rd[kPairs];
   u32x2_t cg[kPairs], cu[kPairs];
   uint32_t bg[kPairs], bu[kPairs];
-  Place at[kPairs];
 #pragma unroll
   for (int b = 0; b < kPairs; ++b) {
-    at[b] = p;
-    const int64_t r = p.r;
-    if (r >= live.lo && r < live.hi) {
-      if constexpr (PACKED) {
-        const int8_t* q = s.q_in + 2 * r * s.I + 8 * p.c;
-        const uint8_t* sc = s.scales_in + 2 * r * s.s_ld + (p.c >> 2);
-        cg[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(q));
-        cu[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(q + s.I));
-        bg[b] = sc[0], bu[b] = sc[s.s_ld];
-      } else {
-        rg[b].load(s.h, r * s.h_ld + 8 * p.c);
-        ru[b].load(s.h, r * s.h_ld + s.I + 8 * p.c);
-      }
-      rd[b].load(s.d_a, r * s.da_ld + 8 * p.c);
+    const Place p = place<MODE, kPairs>(sh, b);
+    if (p.r < live.lo || p.r >= live.hi || p.c >= I8) continue;
+    if constexpr (PACKED) {
+      const int8_t* q = s.q_in + 2 * p.r * s.I + 8 * p.c;
+      const uint8_t* sc = s.scales_in + 2 * p.r * s.s_ld + (p.c >> 2);
+      cg[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(q));
+      cu[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(q + s.I));
+      bg[b] = sc[0], bu[b] = sc[s.s_ld];
+    } else {
+      rg[b].load(s.h, p.r * s.h_ld + 8 * p.c);
+      ru[b].load(s.h, p.r * s.h_ld + s.I + 8 * p.c);
     }
-    advance(p, step, I8);
+    rd[b].load(s.d_a, p.r * s.da_ld + 8 * p.c);
   }
 #pragma unroll
   for (int b = 0; b < kPairs; ++b) {
-    const int64_t r = at[b].r;
-    if (r < live.lo || r >= live.hi) continue;
+    const Place p = place<MODE, kPairs>(sh, b);
+    if (p.r < live.lo || p.r >= live.hi || p.c >= I8) continue;
     float g[8], u[8], d[8], dg[8], a[8];
-    if constexpr (PACKED) decode(cg[b], bg[b], g), decode(cu[b], bu[b], u);
+    if constexpr (PACKED) decode(cg[b], step_of(bg[b]), g), decode(cu[b], step_of(bu[b]), u);
     else rg[b].get(g), ru[b].get(u);
     rd[b].get(d);
 #pragma unroll
@@ -241,71 +274,68 @@ __global__ __launch_bounds__(256) void swiglu_grad(SwigluParams s, bool small) {
       dg[k] = d[k] * u[k] * sg * (1.0f + g[k] * (1.0f - sg));
       d[k] *= silu;
     }
-    const int64_t h = r * s.dh_ld + 8 * at[b].c;
+    const int64_t h = p.r * s.dh_ld + 8 * p.c;
     store8<TYPE>(s.d_h, h, dg);
     store8<TYPE>(s.d_h, h + s.I, d);
-    if (s.a) store8<TYPE>(s.a, r * s.a_ld + 8 * at[b].c, a);
+    if (s.a) store8<TYPE>(s.a, p.r * s.a_ld + 8 * p.c, a);
   }
 }
 
-// Workgroups for `groups` groups of 8, or 0 where they are too many for a grid.
-unsigned blocks_for(int64_t groups, int each) {
-  const int64_t g = (groups + 256 * each - 1) / (256 * each);
-  return g > 0x7FFFFFFF ? 0u : (unsigned)g;
+// f(TYPE, MODE) for a call's type and shape.
+template <class F>
+hipError_t choose(int type, const Shape& s, F&& f) {
+  using std::integral_constant;
+  if (!s.blocks) return hipErrorInvalidConfiguration;
+  auto by_mode = [&](auto ty) {
+    if (s.mode == NARROW) f(ty, integral_constant<int, NARROW>{});
+    else if (s.mode == ROWS) f(ty, integral_constant<int, ROWS>{});
+    else f(ty, integral_constant<int, WIDE>{});
+  };
+  if (type == TYPE_BF16) by_mode(integral_constant<int, TYPE_BF16>{});
+  else if (type == TYPE_F16) by_mode(integral_constant<int, TYPE_F16>{});
+  else by_mode(integral_constant<int, TYPE_F32>{});
+  return hipGetLastError();
 }
-bool is_small(int64_t groups) { return groups < 0x7FFFFFFF - 4096; }
+// Lanes of a row whose blocks of 32 are found by four lanes each.
+int quads(int n8) { return (n8 + 3) & ~3; }
 
 }  // namespace
 
 hipError_t launch_mx8_quant(const void* x, int type, int64_t rows, int K, int64_t ld, int8_t* q, uint8_t* scales,
                             int s_ld, hipStream_t s) {
-  const int K8 = K / 8;
-  const int64_t n = rows * ((K8 + 3) & ~3);
-  const unsigned g = blocks_for(n, kBatch);
-  const bool small = is_small(n);
-  if (!g) return hipErrorInvalidConfiguration;
-  if (type == TYPE_BF16) mx8_quant<TYPE_BF16><<<g, 256, 0, s>>>(x, rows, K8, ld, q, scales, s_ld, small);
-  else if (type == TYPE_F16) mx8_quant<TYPE_F16><<<g, 256, 0, s>>>(x, rows, K8, ld, q, scales, s_ld, small);
-  else mx8_quant<TYPE_F32><<<g, 256, 0, s>>>(x, rows, K8, ld, q, scales, s_ld, small);
-  return hipGetLastError();
+  const Shape sh = shape_of(rows, quads(K / 8), kQuant);
+  return choose(type, sh, [&](auto ty, auto mode) {
+    mx8_quant<decltype(ty)::value, decltype(mode)::value><<<sh.blocks, 256, 0, s>>>(x, rows, K / 8, ld, q, scales, s_ld,
+                                                                                    sh);
+  });
 }
 
 hipError_t launch_mx8_dequant(const Mx8Rows& p, int type, hipStream_t s) {
-  const int64_t n = p.out_rows * (p.K / 8);
-  const unsigned g = blocks_for(n, kBatch);
-  const bool small = is_small(n);
-  if (!g) return hipErrorInvalidConfiguration;
-  if (type == TYPE_BF16) mx8_dequant<TYPE_BF16><<<g, 256, 0, s>>>(p, small);
-  else if (type == TYPE_F16) mx8_dequant<TYPE_F16><<<g, 256, 0, s>>>(p, small);
-  else mx8_dequant<TYPE_F32><<<g, 256, 0, s>>>(p, small);
-  return hipGetLastError();
+  Shape sh = shape_of(p.out_rows, p.K / 8, kDequant);
+  const bool many = sh.mode == WIDE && p.row_src && sh.blocks >= 4096;
+  if (many) sh = shape_of((p.out_rows + kRoutedRows - 1) / kRoutedRows, p.K / 8, kDequant);
+  return choose(type, sh, [&](auto ty, auto mode) {
+    constexpr int TYPE = decltype(ty)::value, MODE = decltype(mode)::value;
+    if constexpr (MODE == WIDE)
+      if (many) return mx8_dequant<TYPE, MODE, kRoutedRows><<<sh.blocks, 256, 0, s>>>(p, sh);
+    mx8_dequant<TYPE, MODE, 1><<<sh.blocks, 256, 0, s>>>(p, sh);
+  });
 }
 
 hipError_t launch_swiglu_save(const SwigluParams& p, int type, hipStream_t s) {
-  const int64_t n = (int64_t)p.rows * ((p.I / 8 + 3) & ~3);
-  const unsigned g = blocks_for(n, kPairs);
-  const bool small = is_small(n);
-  if (!g) return hipErrorInvalidConfiguration;
-  if (type == TYPE_BF16) swiglu_save<TYPE_BF16><<<g, 256, 0, s>>>(p, small);
-  else if (type == TYPE_F16) swiglu_save<TYPE_F16><<<g, 256, 0, s>>>(p, small);
-  else swiglu_save<TYPE_F32><<<g, 256, 0, s>>>(p, small);
-  return hipGetLastError();
-}
-
-template <bool PACKED>
-static hipError_t grad_for(const SwigluParams& p, int type, hipStream_t s) {
-  const int64_t n = (int64_t)p.rows * (p.I / 8);
-  const unsigned g = blocks_for(n, kPairs);
-  const bool small = is_small(n);
-  if (!g) return hipErrorInvalidConfiguration;
-  if (type == TYPE_BF16) swiglu_grad<TYPE_BF16, PACKED><<<g, 256, 0, s>>>(p, small);
-  else if (type == TYPE_F16) swiglu_grad<TYPE_F16, PACKED><<<g, 256, 0, s>>>(p, small);
-  else swiglu_grad<TYPE_F32, PACKED><<<g, 256, 0, s>>>(p, small);
-  return hipGetLastError();
+  const Shape sh = shape_of(p.rows, quads(p.I / 8), kPairs);
+  return choose(type, sh, [&](auto ty, auto mode) {
+    swiglu_save<decltype(ty)::value, decltype(mode)::value><<<sh.blocks, 256, 0, s>>>(p, sh);
+  });
 }
 
 hipError_t launch_swiglu_grad(const SwigluParams& p, int type, hipStream_t s) {
-  return p.h ? grad_for<false>(p, type, s) : grad_for<true>(p, type, s);
+  const Shape sh = shape_of(p.rows, p.I / 8, kPairs);
+  return choose(type, sh, [&](auto ty, auto mode) {
+    constexpr int TYPE = decltype(ty)::value, MODE = decltype(mode)::value;
+    if (p.h) swiglu_grad<TYPE, MODE, false><<<sh.blocks, 256, 0, s>>>(p, sh);
+    else swiglu_grad<TYPE, MODE, true><<<sh.blocks, 256, 0, s>>>(p, sh);
+  });
 }
 
 }  // namespace moe

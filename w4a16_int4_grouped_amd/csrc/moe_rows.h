@@ -64,20 +64,27 @@ struct Raw8 {
   }
 };
 
-template <int TYPE>
+// PAST: past the caches.
+template <bool PAST, class V>
+__device__ __forceinline__ void store_vec(void* p, V v) {
+  if constexpr (PAST) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else *static_cast<V*>(p) = v;
+}
+template <int TYPE, bool PAST = false>
 __device__ __forceinline__ void store8(void* x, int64_t at, const float (&v)[8]) {
   if constexpr (TYPE == TYPE_F32) {
     f32x4_t* p = reinterpret_cast<f32x4_t*>(static_cast<float*>(x) + at);
-    p[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-    p[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+    store_vec<PAST>(p, f32x4_t{v[0], v[1], v[2], v[3]});
+    store_vec<PAST>(p + 1, f32x4_t{v[4], v[5], v[6], v[7]});
   } else if constexpr (TYPE == TYPE_BF16) {
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(x) + at) =
-        u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    store_vec<PAST>(static_cast<uint16_t*>(x) + at,
+                    u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                            pack_bf16x2(v[6], v[7])});
   } else {
     f16x8_t h;
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
-    *reinterpret_cast<f16x8_t*>(static_cast<_Float16*>(x) + at) = h;
+    store_vec<PAST>(static_cast<_Float16*>(x) + at, h);
   }
 }
 

@@ -17,78 +17,74 @@ namespace {
 
 constexpr int kRowsAhead = 8;   // rows whose loads are in flight together
 
-// A thread sums 8 columns of a token. 1 << lg threads (a power of two, at most
-// 256) lie along a row, nb times where the row is longer.
-template <int TYPE>
-__global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type, int lg, int nb) {
-  const int blk = blockIdx.x / nb, cb = blockIdx.x - blk * nb;
-  const int64_t t = (int64_t)blk * (256 >> lg) + (threadIdx.x >> lg);
-  const int col = 8 * (cb * 256 + (threadIdx.x & ((1 << lg) - 1)));
-  if (t >= p.T || col >= p.H) return;
-  float acc[8] = {};
+// A thread sums 8 columns of a token at a time. 1 << lg threads (a power of two,
+// at most 256) lie along a row; where it is longer, `parts` workgroups share it
+// and go through their columns one block of 2048 after another. ROW: a wave's
+// lanes have one token, whose slots and weights are scalars.
+template <int TYPE, bool ROW>
+__global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type, int lg, int parts) {
+  const int blk = parts == 1 ? blockIdx.x : blockIdx.x / parts, part = blockIdx.x - blk * parts;
+  const int row = threadIdx.x >> lg;
+  const int64_t t = (int64_t)blk * (256 >> lg) + (ROW ? __builtin_amdgcn_readfirstlane(row) : row);
+  if (t >= p.T) return;
   const int32_t* slots = p.slots + t * p.topk;
-  for (int j0 = 0; j0 < p.topk; j0 += kRowsAhead) {
-    int slot[kRowsAhead];
-    float w[kRowsAhead];
-    Raw8<TYPE> raw[kRowsAhead];
+  for (int col = 8 * (part * 256 + (threadIdx.x & ((1 << lg) - 1))); col < p.H; col += 2048 * parts) {
+    float acc[8] = {};
+    for (int j0 = 0; j0 < p.topk; j0 += kRowsAhead) {
+      int slot[kRowsAhead];
+      float w[kRowsAhead];
+      Raw8<TYPE> raw[kRowsAhead];
 #pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j) {
-      const bool in = j0 + j < p.topk;
-      slot[j] = in ? slots[j0 + j] : -1;
-      w[j] = in && p.w ? p.w[t * p.topk + j0 + j] : 1.f;
+      for (int j = 0; j < kRowsAhead; ++j) {
+        const bool in = j0 + j < p.topk;
+        slot[j] = in ? slots[j0 + j] : -1;
+        w[j] = in && p.w ? p.w[t * p.topk + j0 + j] : 1.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j) {
+        raw[j].zero();
+        if (slot[j] >= 0 && slot[j] < p.R) raw[j].load(p.y, slot[j] * p.y_ld + col);
+      }
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j) {
+        if (slot[j] < 0 || slot[j] >= p.R) continue;
+        float v[8];
+        raw[j].get(v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(w[j], v[k], acc[k]);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j) {
-      raw[j].zero();
-      if (slot[j] >= 0 && slot[j] < p.R) raw[j].load(p.y, slot[j] * p.y_ld + col);
-    }
-#pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j) {
-      if (slot[j] < 0 || slot[j] >= p.R) continue;
-      float v[8];
-      raw[j].get(v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(w[j], v[k], acc[k]);
-    }
+    const int64_t at = t * p.out_ld + col;
+    if (out_type == TYPE_BF16) store8<TYPE_BF16>(p.out, at, acc);
+    else if (out_type == TYPE_F16) store8<TYPE_F16>(p.out, at, acc);
+    else store8<TYPE_F32>(p.out, at, acc);
   }
-  const int64_t at = t * p.out_ld + col;
-  if (out_type == TYPE_BF16) store8<TYPE_BF16>(p.out, at, acc);
-  else if (out_type == TYPE_F16) store8<TYPE_F16>(p.out, at, acc);
-  else store8<TYPE_F32>(p.out, at, acc);
 }
 
 constexpr int kHeld = 4;        // pieces of 8 values of d_out that a thread holds
 
-// TEAM threads (64 or 256) take `each` of a token's rows. Workgroups behind
-// those of the tokens look through 64 rows each for such as no token names and
-// write 0 there.
+constexpr int kPadRows = 16;
+
+// TEAM threads (64 or 256) take `each` of a token's rows. The first workgroups
+// look through kPadRows rows each for such as no token names and write 0 there.
 template <int TYPE, int TEAM>
-__global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, int each, int teams_blocks) {
+__global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, int each, int pad_blocks) {
   __shared__ float sums[4][64];   // of a wave, per row
-  __shared__ int pad[64];
-  __shared__ int pads;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if ((int)blockIdx.x >= teams_blocks) {
+  if ((int)blockIdx.x < pad_blocks) {
     const int lo = p.offsets ? max(p.offsets[0], 0) : 0, hi = p.offsets ? min(p.offsets[p.E], p.R) : p.R;
-    const int r0 = ((int)blockIdx.x - teams_blocks) * 64;
-    if (threadIdx.x < 64) {
-      const int r = r0 + lane;
-      bool none = false;
-      if (r >= lo && r < hi) {
-        const int src = p.row_src[r];
-        none = src < 0 || (int64_t)src >= (int64_t)p.T * p.topk;
-      }
-      const uint64_t m = __ballot(none);
-      if (none) pad[__popcll(m & ((1ull << lane) - 1))] = r;
-      if (lane == 0) pads = __popcll(m);
-    }
-    __syncthreads();
     const float zero[8] = {};
-    for (int i = wave; i < pads; i += 4)
-      for (int c = 8 * lane; c < p.H; c += 512) store8<TYPE>(p.d_y, pad[i] * p.dy_ld + c, zero);
+    for (int i = wave; i < kPadRows; i += 4) {
+      const int64_t r = (int64_t)blockIdx.x * kPadRows + i;
+      if (r < lo || r >= hi) continue;
+      const int src = p.row_src[r];
+      if (src >= 0 && (int64_t)src < (int64_t)p.T * p.topk) continue;
+      for (int c = 8 * lane; c < p.H; c += 512) store8<TYPE, true>(p.d_y, r * p.dy_ld + c, zero);
+    }
     return;
   }
-  const int team = TEAM == 64 ? blockIdx.x * 4 + wave : blockIdx.x;
+  const int block = (int)blockIdx.x - pad_blocks;
+  const int team = TEAM == 64 ? block * 4 + wave : block;
   const int64_t t = team / parts;
   const int id = TEAM == 64 ? lane : threadIdx.x;
   if (t < p.T) {
@@ -131,7 +127,7 @@ __global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, 
           float v[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = w * d[i][k];
-          store8<TYPE>(p.d_y, slot * p.dy_ld + cols[i], v);
+          store8<TYPE, true>(p.d_y, slot * p.dy_ld + cols[i], v);
         }
         if (p.y) {
           const float sum = wave_sum_of(dot);
@@ -160,12 +156,17 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
   const int H8 = p.H / 8;
   int lg = 0;
   while (lg < 8 && (1 << lg) < H8) ++lg;
-  const int nb = (H8 + 255) / 256;
-  const int64_t g = ((int64_t)p.T + (256 >> lg) - 1) / (256 >> lg) * nb;
+  const int parts = p.T >= 2048 ? 1 : (H8 + 255) / 256;
+  const int64_t g = ((int64_t)p.T + (256 >> lg) - 1) / (256 >> lg) * parts;
   if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  if (type == TYPE_BF16) combine_sum<TYPE_BF16><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, nb);
-  else if (type == TYPE_F16) combine_sum<TYPE_F16><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, nb);
-  else combine_sum<TYPE_F32><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, nb);
+  auto go = [&](auto ty) {
+    constexpr int TYPE = decltype(ty)::value;
+    if (lg >= 6) combine_sum<TYPE, true><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
+    else combine_sum<TYPE, false><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
+  };
+  if (type == TYPE_BF16) go(std::integral_constant<int, TYPE_BF16>{});
+  else if (type == TYPE_F16) go(std::integral_constant<int, TYPE_F16>{});
+  else go(std::integral_constant<int, TYPE_F32>{});
   return hipGetLastError();
 }
 
@@ -174,13 +175,14 @@ hipError_t launch_combine_grad(const CombineParams& p, int type, hipStream_t s) 
   // few tokens: their rows one by one
   const int parts = p.T >= 1024 ? 1 : p.topk, each = p.T >= 1024 ? p.topk : 1;
   const int64_t teams = (int64_t)p.T * parts, blocks = wide ? teams : (teams + 3) / 4;
-  const int64_t g = blocks + (p.row_src ? (p.R + 63) / 64 : 0);
+  const int pads = p.row_src ? (p.R + kPadRows - 1) / kPadRows : 0;
+  const int64_t g = blocks + pads;
   if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   if (g == 0) return hipSuccess;
   auto go = [&](auto ty) {
     constexpr int TYPE = decltype(ty)::value;
-    if (wide) combine_grad<TYPE, 256><<<(unsigned)g, 256, 0, s>>>(p, parts, each, (int)blocks);
-    else combine_grad<TYPE, 64><<<(unsigned)g, 256, 0, s>>>(p, parts, each, (int)blocks);
+    if (wide) combine_grad<TYPE, 256><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
+    else combine_grad<TYPE, 64><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
   };
   if (type == TYPE_BF16) go(std::integral_constant<int, TYPE_BF16>{});
   else if (type == TYPE_F16) go(std::integral_constant<int, TYPE_F16>{});
