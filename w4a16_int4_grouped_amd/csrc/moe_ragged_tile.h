@@ -358,15 +358,13 @@ __device__ __forceinline__ f32x4_t bias4(const Epilogue& x, int e, int col) {
   return load4(x.bias, (int64_t)e * x.bias_ld + col, x.bias_type);
 }
 
-// N values (16 bytes) of a row of the residual, added to v.
+// 16 bytes of a row of the residual, added to v.
 template <int TYPE>
-__device__ __forceinline__ void add_residual(const void* res, int64_t at, float* v) {
+__device__ __forceinline__ void add_residual(const u32x4_t& w, float* v) {
   if constexpr (TYPE == TYPE_F32) {
-    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(res) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += w[i];
+    for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(w[i]);
   } else {
-    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(res) + at);
     const f16x8_t h = __builtin_bit_cast(f16x8_t, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -660,8 +658,9 @@ struct TileBody {
     }
   }
 
-  // The same with a residual: turned in FP32, 16 bytes of the output a lane.
-  template <int TYPE>
+  // The same with a residual: turned in FP32, 16 bytes of the output a lane. The
+  // residual of 32 rows is read before they are turned.
+  template <int TYPE, bool PAST>
   __device__ __forceinline__ void store_onto(const RaggedParams& p, int64_t row0, int i0, int ni, int nj) {
     constexpr int kW = BO / WI, kSize = TYPE == TYPE_F32 ? 4 : 2, kV = 16 / kSize;
     constexpr int kPitch = kW * 4 + 16;
@@ -671,6 +670,15 @@ struct TileBody {
     const int col = wi * kW + (lane % kLanes) * kV;
 #pragma unroll
     for (int u = 0; u < TJ; ++u) {
+      u32x4_t res[32 / kRows];
+#pragma unroll
+      for (int r = 0; r < 32; r += kRows) {
+        const int jj = wj * (BJ / WJ) + 32 * u + r + lane / kLanes;
+        const u32x4_t* at = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p.epi.res) +
+                                                             ((row0 + jj) * p.epi.res_ld + i0 + col) * kSize);
+        res[r / kRows] = u32x4_t{};
+        if (jj < nj && col < ni) res[r / kRows] = PAST ? __builtin_nontemporal_load(at) : *at;
+      }
 #pragma unroll
       for (int t = 0; t < TO; ++t)
 #pragma unroll
@@ -683,19 +691,23 @@ struct TileBody {
 #pragma unroll
       for (int r = 0; r < 32; r += kRows) {
         const int j = r + lane / kLanes, jj = wj * (BJ / WJ) + 32 * u + j;
-        if (jj < nj && col < ni) {
-          float v[kV];
-          const f32x4_t* at = reinterpret_cast<const f32x4_t*>(buf + j * kPitch + (lane % kLanes) * kV * 4);
+        float v[kV];
+        const f32x4_t* from = reinterpret_cast<const f32x4_t*>(buf + j * kPitch + (lane % kLanes) * kV * 4);
 #pragma unroll
-          for (int i = 0; i < kV; ++i) v[i] = at[i / 4][i % 4];
-          add_residual<TYPE>(p.epi.res, (row0 + jj) * p.epi.res_ld + i0 + col, v);
-char* out = static_cast<char*>(p.out) + ((row0 + jj) * p.out_ld + i0 + col) * kSize;
-          if constexpr (TYPE == TYPE_F32) {
-            *reinterpret_cast<f32x4_t*>(out) = f32x4_t{v[0], v[1], v[2], v[3]};
-          } else {
-            const u32x2_t lo = pack4<TYPE>(v[0], v[1], v[2], v[3]), hi = pack4<TYPE>(v[4], v[5], v[6], v[7]);
-            *reinterpret_cast<u32x4_t*>(out) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-          }
+        for (int i = 0; i < kV; ++i) v[i] = from[i / 4][i % 4];
+        add_residual<TYPE>(res[r / kRows], v);
+        u32x4_t w;
+        if constexpr (TYPE == TYPE_F32) {
+          w = __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]});
+        } else {
+          const u32x2_t lo = pack4<TYPE>(v[0], v[1], v[2], v[3]), hi = pack4<TYPE>(v[4], v[5], v[6], v[7]);
+          w = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+        }
+        if (jj < nj && col < ni) {
+          u32x4_t* at = reinterpret_cast<u32x4_t*>(static_cast<char*>(p.out) +
+                                                   ((row0 + jj) * p.out_ld + i0 + col) * kSize);
+          if constexpr (PAST) __builtin_nontemporal_store(w, at);
+          else *at = w;
         }
       }
       __builtin_amdgcn_wave_barrier();
@@ -729,14 +741,20 @@ char* out = static_cast<char*>(p.out) + ((row0 + jj) * p.out_ld + i0 + col) * kS
     fence<0>();   // every wave is past its last fragments
     if constexpr (EPI != EPI_NONE) {
       if (p.epi.res) {
-        if (p.out_type == TYPE_BF16) store_onto<TYPE_BF16>(p, row0, i0, ni, nj);
-        else if (p.out_type == TYPE_F16) store_onto<TYPE_F16>(p, row0, i0, ni, nj);
-        else store_onto<TYPE_F32>(p, row0, i0, ni, nj);
+        if (p.stream_out) onto_any<true>(p, row0, i0, ni, nj);
+        else onto_any<false>(p, row0, i0, ni, nj);
         return;
       }
     }
     if (p.stream_out) store_any<true>(p, base, row0, i0, ni, nj);
     else store_any<false>(p, base, row0, i0, ni, nj);
+  }
+
+  template <bool PAST>
+  __device__ __forceinline__ void onto_any(const RaggedParams& p, int64_t row0, int i0, int ni, int nj) {
+    if (p.out_type == TYPE_BF16) store_onto<TYPE_BF16, PAST>(p, row0, i0, ni, nj);
+    else if (p.out_type == TYPE_F16) store_onto<TYPE_F16, PAST>(p, row0, i0, ni, nj);
+    else store_onto<TYPE_F32, PAST>(p, row0, i0, ni, nj);
   }
 
   template <bool PAST>
