@@ -538,15 +538,22 @@ moe_status_t moe_grouped_linear(const void* a, int64_t a_ld, const void* w, int6
                                 const void* residual, int64_t res_ld, void* out, int64_t out_ld,
                                 int32_t out_dtype, moe_stream_t stream);
 
+/* Bytes of moe_grouped_bias_grad's workspace: 0 where it needs none, -1 for
+ * sizes outside its limits. */
+int64_t moe_grouped_bias_grad_bytes(int32_t E, int32_t M, int32_t N);
+
 /* Gradient of the biases: db[e] = sum over the rows r of e of dy[r]; 0 for an
  * expert without rows.
  *   dy   device [M, N] of dtype (BF16 or FP16), db device [E, N] of out_dtype,
  *        rows db_ld values apart, fully written
- * Otherwise as moe_grouped_gemm. */
+ *   ws   device, 16-byte aligned, of ws_bytes >= moe_grouped_bias_grad_bytes
+ *        (NULL if that is 0); nothing in it has to be kept or cleared
+ * Enqueues one kernel, or two where few groups have many rows. Otherwise as
+ * moe_grouped_gemm; also WORKSPACE_TOO_SMALL. */
 moe_status_t moe_grouped_bias_grad(const void* dy, int64_t dy_ld, int32_t dtype,
                                    const int32_t* offsets, int32_t E, int32_t M, int32_t N,
-                                   void* db, int64_t db_ld, int32_t out_dtype,
-                                   moe_stream_t stream);
+                                   void* db, int64_t db_ld, int32_t out_dtype, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream);
 
 /* ---- operators of a training step -------------------------------------------
  *

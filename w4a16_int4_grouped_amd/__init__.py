@@ -55,7 +55,7 @@ EXPORTS = [
     "moe_profile_enable", "moe_profile_reset", "moe_profile_read",
     "moe_router_balance_bytes", "moe_router_balance", "moe_router_balance_grad", "moe_combine", "moe_combine_grad",
     "moe_mx8_scale_cols", "moe_mx8_quant", "moe_mx8_dequant", "moe_swiglu_save", "moe_swiglu_grad",
-    "moe_grouped_linear", "moe_grouped_bias_grad",
+    "moe_grouped_linear", "moe_grouped_bias_grad_bytes", "moe_grouped_bias_grad",
 ]
 
 
@@ -152,7 +152,8 @@ def lib() -> ctypes.CDLL:
         "moe_swiglu_save": (S, [P, I32, I64, I32, I32, P, I32, P, I64, P, P, P]),
         "moe_grouped_linear": (S, [P, I64, P, I64, I64, I32, P, I32, I32, I32, I32, P, I32, I64, I32, P, I64, P, I64, I32,
                                    P]),
-        "moe_grouped_bias_grad": (S, [P, I64, I32, P, I32, I32, I32, P, I64, I32, P]),
+        "moe_grouped_bias_grad_bytes": (I64, [I32, I32, I32]),
+        "moe_grouped_bias_grad": (S, [P, I64, I32, P, I32, I32, I32, P, I64, I32, P, SZ, P]),
         "moe_swiglu_grad": (S, [P, I64, P, P, I32, I32, I32, P, I64, P, I32, P, I64, P, I64, P]),
         "moe_profile_enable": (S, [S]),
         "moe_profile_reset": (None, []),
@@ -667,10 +668,19 @@ def grouped_linear(a, w, offsets, bias=None, act="none", residual=None, out=None
     return out
 
 
-def grouped_bias_grad(dy, offsets, out=None, out_dtype=None, stream=None):
+@functools.lru_cache(maxsize=256)
+def _bias_grad_bytes(E, M, N) -> int:
+    n = lib().moe_grouped_bias_grad_bytes(E, M, N)
+    if n < 0:
+        check(MOE_ERR_INVALID_ARG)
+    return n
+
+
+def grouped_bias_grad(dy, offsets, out=None, out_dtype=None, ws=None, stream=None):
     """Gradient of grouped_linear's bias: out[e] = the sum of dy's rows of e,
     [E, N] of out_dtype (default dy's; fp32 as well); 0 for an expert without
-    rows. dy [M, N] bf16 or fp16, N a multiple of 8."""
+    rows. dy [M, N] bf16 or fp16, N a multiple of 8. `ws` may give a uint8
+    workspace."""
     if _torch is None:
         _load()
     _need(dy.dim() == 2, "dy: [M, N]")
@@ -685,8 +695,15 @@ def grouped_bias_grad(dy, offsets, out=None, out_dtype=None, stream=None):
         o_ld = N
     else:
         o_ld = _matrix(out, "out", out_dtype, dev, (E, N))
+    nbytes = _bias_grad_bytes(E, M, N)
+    if ws is not None:
+        nbytes = ws.numel()
+        _dense(ws, "ws", _torch.uint8, dev, (nbytes,))
+    elif nbytes:
+        ws = _empty(nbytes, dev, stream)
     _call((_lib or lib()).moe_grouped_bias_grad, dev, stream,
-          dy.data_ptr(), y_ld, _dtype(dy.dtype), off, E, M, N, out.data_ptr(), o_ld, _dtype(out.dtype))
+          dy.data_ptr(), y_ld, _dtype(dy.dtype), off, E, M, N, out.data_ptr(), o_ld, _dtype(out.dtype),
+          None if ws is None else ws.data_ptr(), nbytes)
     return out
 
 
@@ -794,6 +811,14 @@ def _offsets(t, device):
     return t.data_ptr(), t.shape[0] - 1
 
 
+@functools.lru_cache(maxsize=256)
+def _balance_bytes(T, E, S) -> int:
+    n = lib().moe_router_balance_bytes(T, E, S)
+    if n == 0:
+        check(MOE_ERR_INVALID_ARG)
+    return n
+
+
 def router_balance(logits, ids, score="softmax", offsets=None, out=None, ws=None, stream=None):
     """(loss float32 [S], counts int32 [S, E]) of S sequences of tokens, rows
     [offsets[s], offsets[s + 1]) of logits [T, E] (bf16, fp16 or fp32) and of
@@ -821,9 +846,7 @@ def router_balance(logits, ids, score="softmax", offsets=None, out=None, ws=None
         _dense(loss, "loss", torch.float32, dev, (S,))
         _dense(counts, "counts", torch.int32, dev, (S, E))
     if ws is None:
-        nbytes = L.moe_router_balance_bytes(T, E, S)
-        if nbytes == 0:
-            check(MOE_ERR_INVALID_ARG)
+        nbytes = _balance_bytes(T, E, S)
         ws = _empty(nbytes, dev, stream)
     else:
         nbytes = ws.numel()

@@ -1,8 +1,13 @@
 // Gradient of the experts' biases: the sum of each group's rows, in FP32.
 //
-// A workgroup sums LANES * 8 columns of one group: LANES lanes lie along a row
-// (16 bytes each), the others and the waves along the rows, whose sums meet in a
-// fixed order. A group's rows are one workgroup's, whatever their number.
+// A workgroup sums 64 columns of one group: 8 lanes lie along a row (16 bytes
+// each, a line), the others and the waves along the rows, whose sums meet in a
+// fixed order. HBM bounds it where there are enough groups and columns: 24576
+// rows of 4096 in 48 groups 34 us (6.0 TB/s). A workgroup alone reads 88 GB/s:
+// where groups are few and long, the rows are cut into chunks, a workgroup sums
+// 64 columns of a chunk for each group in it, and a second kernel adds the
+// chunks' sums up. Part c + e of the workspace belongs to chunk c and group e; no
+// two such pairs have the same sum, because both only grow along the rows.
 #include "moe_rows.h"
 #include "moe_step.h"
 
@@ -10,19 +15,25 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kAhead = 4;   // rows of a lane whose loads are in flight together
+constexpr int kAhead = 4;    // rows of a lane whose loads are in flight together
+constexpr int kChunk = 256;  // rows: a round of loads
 
-template <int TYPE, int LANES>
-__global__ __launch_bounds__(64 * kWaves) void bias_grad(BiasGradParams p, int out_type, int blocks) {
-  __shared__ float part[kWaves][LANES * 8];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.x / blocks, c0 = (blockIdx.x - e * blocks) * LANES * 8;
-  const int col = c0 + 8 * (lane % LANES);
-  const int lo = min(max(p.offsets[e], 0), p.M), hi = min(p.offsets[e + 1], p.M);
+struct Rows {
+  int lo, hi;
+};
+__device__ __forceinline__ Rows group(const BiasGradParams& p, int e) {
+  const int lo = min(max(p.offsets[e], 0), p.M);
+  return Rows{lo, max(min(p.offsets[e + 1], p.M), lo)};
+}
+
+// The sum of column c0 + threadIdx.x over rows [lo, hi), in threads below 64.
+template <int TYPE>
+__device__ __forceinline__ float column_sum(const BiasGradParams& p, int c0, int lo, int hi, float (&part)[kWaves][64]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = c0 + 8 * (lane & 7);
   float sum[8] = {};
   if (col < p.N) {
-    constexpr int kStep = 64 / LANES * kWaves;   // rows of a round
-    for (int64_t r = lo + wave * (64 / LANES) + lane / LANES; r < hi; r += kStep * kAhead) {
+    constexpr int kStep = 8 * kWaves;   // rows of a round
+    for (int64_t r = lo + wave * 8 + (lane >> 3); r < hi; r += kStep * kAhead) {
       Raw8<TYPE> raw[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
@@ -41,39 +52,109 @@ __global__ __launch_bounds__(64 * kWaves) void bias_grad(BiasGradParams p, int o
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
 #pragma unroll
-    for (int o = LANES; o < 64; o <<= 1) sum[k] += __shfl_xor(sum[k], o, 64);
+    for (int o = 8; o < 64; o <<= 1) sum[k] += __shfl_xor(sum[k], o, 64);
   }
-  if (lane < LANES) {
+  if (lane < 8) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) part[wave][8 * lane + k] = sum[k];
   }
   __syncthreads();
-  const int c = threadIdx.x;
-  if (c >= LANES * 8 || c0 + c >= p.N) return;
   float v = 0.f;
+  if (threadIdx.x < 64) {
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) v += part[w][c];
-  const int64_t at = (int64_t)e * p.db_ld + c0 + c;
-  if (out_type == TYPE_BF16) store1<TYPE_BF16>(p.db, at, v);
-  else if (out_type == TYPE_F16) store1<TYPE_F16>(p.db, at, v);
-  else store1<TYPE_F32>(p.db, at, v);
+    for (int w = 0; w < kWaves; ++w) v += part[w][threadIdx.x];
+  }
+  return v;
 }
 
-template <int TYPE, int LANES>
-hipError_t go(const BiasGradParams& p, int out_type, hipStream_t s) {
-  const int blocks = (p.N + LANES * 8 - 1) / (LANES * 8);
-  const int64_t g = (int64_t)p.E * blocks;
-  if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  bias_grad<TYPE, LANES><<<(unsigned)g, 64 * kWaves, 0, s>>>(p, out_type, blocks);
-  return hipGetLastError();
+__device__ __forceinline__ void store_any(void* x, int64_t at, int type, float v) {
+  if (type == TYPE_BF16) store1<TYPE_BF16>(x, at, v);
+  else if (type == TYPE_F16) store1<TYPE_F16>(x, at, v);
+  else store1<TYPE_F32>(x, at, v);
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(64 * kWaves) void bias_grad(BiasGradParams p, int out_type, int blocks) {
+  __shared__ float part[kWaves][64];
+  const int e = blockIdx.x / blocks, c0 = (blockIdx.x - e * blocks) * 64;
+  const Rows g = group(p, e);
+  const float v = column_sum<TYPE>(p, c0, g.lo, g.hi, part);
+  if (threadIdx.x < 64 && c0 + (int)threadIdx.x < p.N)
+    store_any(p.db, (int64_t)e * p.db_ld + c0 + threadIdx.x, out_type, v);
+}
+
+// Chunk blockIdx.x / blocks; the groups in it, the first found by halves.
+template <int TYPE>
+__global__ __launch_bounds__(64 * kWaves) void bias_grad_parts(BiasGradParams p, int blocks) {
+  __shared__ float part[kWaves][64];
+  const int c = blockIdx.x / blocks, c0 = (blockIdx.x - c * blocks) * 64;
+  const int r0 = c * kChunk, r1 = min((int64_t)r0 + kChunk, (int64_t)p.M);
+  int a = 0, b = p.E;
+  while (a < b) {
+    const int m = (a + b) / 2;
+    if (p.offsets[m + 1] > r0) b = m;
+    else a = m + 1;
+  }
+  for (int e = a; e < p.E; ++e) {
+    const Rows g = group(p, e);
+    if (g.lo >= r1) break;
+    const int lo = max(g.lo, r0), hi = min(g.hi, r1);
+    if (lo >= hi) continue;
+    const float v = column_sum<TYPE>(p, c0, lo, hi, part);
+    if (threadIdx.x < 64 && c0 + (int)threadIdx.x < p.N)
+      static_cast<float*>(p.ws)[((int64_t)c + e) * p.N + c0 + threadIdx.x] = v;
+    __syncthreads();
+  }
+}
+
+__global__ __launch_bounds__(64 * kWaves) void bias_grad_finish(BiasGradParams p, int out_type, int blocks) {
+  __shared__ float part[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x / blocks, col = (blockIdx.x - e * blocks) * 64 + lane;
+  const Rows g = group(p, e);
+  float v = 0.f;
+  if (g.lo < g.hi && col < p.N) {
+    const float* from = static_cast<const float*>(p.ws) + (int64_t)e * p.N + col;
+#pragma unroll 8
+    for (int c = g.lo / kChunk + wave; c <= (g.hi - 1) / kChunk; c += kWaves) v += from[(int64_t)c * p.N];
+  }
+  part[wave][lane] = v;
+  __syncthreads();
+  if (wave || col >= p.N) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) v += part[w][lane];
+  store_any(p.db, (int64_t)e * p.db_ld + col, out_type, v);
+}
+
+int64_t chunks_of(int M) { return ((int64_t)M + kChunk - 1) / kChunk; }
+
+// Whether the rows are cut: an even group's time in one workgroup, and no less
+// than all bytes at 5.5 TB/s, against those bytes and a second kernel's 4 us.
+bool cut(int E, int M, int N) {
+  const double rows = (double)M / E, waves = (double)E * ((N + 63) / 64) / 512, bytes = (double)M * N * 2 / 5.5e6;
+  const double alone = rows * 128 / 88e3 * (waves > 1 ? waves : 1);
+  return (alone > bytes ? alone : bytes) > bytes + 4;
 }
 
 }  // namespace
 
+size_t bias_grad_ws_bytes(int E, int M, int N) { return cut(E, M, N) ? (size_t)(chunks_of(M) + E) * N * 4 : 0; }
+
 hipError_t launch_bias_grad(const BiasGradParams& p, int type, int out_type, hipStream_t s) {
-  const bool wide = (int64_t)p.E * ((p.N + 63) / 64) >= 256;   // workgroups for every CU
-  if (type == TYPE_BF16) return wide ? go<TYPE_BF16, 8>(p, out_type, s) : go<TYPE_BF16, 1>(p, out_type, s);
-  return wide ? go<TYPE_F16, 8>(p, out_type, s) : go<TYPE_F16, 1>(p, out_type, s);
+  const int blocks = (p.N + 63) / 64;
+  const int64_t groups = (int64_t)p.E * blocks, parts = chunks_of(p.M) * blocks;
+  if (groups > 0x7FFFFFFF || parts > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (!cut(p.E, p.M, p.N)) {
+    if (type == TYPE_BF16) bias_grad<TYPE_BF16><<<(unsigned)groups, 64 * kWaves, 0, s>>>(p, out_type, blocks);
+    else bias_grad<TYPE_F16><<<(unsigned)groups, 64 * kWaves, 0, s>>>(p, out_type, blocks);
+    return hipGetLastError();
+  }
+  if (type == TYPE_BF16) bias_grad_parts<TYPE_BF16><<<(unsigned)parts, 64 * kWaves, 0, s>>>(p, blocks);
+  else bias_grad_parts<TYPE_F16><<<(unsigned)parts, 64 * kWaves, 0, s>>>(p, blocks);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  bias_grad_finish<<<(unsigned)groups, 64 * kWaves, 0, s>>>(p, out_type, blocks);
+  return hipGetLastError();
 }
 
 }  // namespace moe

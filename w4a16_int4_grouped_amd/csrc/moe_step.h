@@ -109,7 +109,9 @@ struct BiasGradParams {
   int E, M, N;
   void* db;                 // [E][db_ld]
   int64_t db_ld;
+  void* ws;                 // of bias_grad_ws_bytes
 };
+size_t bias_grad_ws_bytes(int E, int M, int N);
 hipError_t launch_bias_grad(const BiasGradParams& p, int type, int out_type, hipStream_t s);
 
 }  // namespace moe

@@ -274,16 +274,29 @@ moe_status_t moe_grouped_linear(const void* a, int64_t a_ld, const void* w, int6
                   "grouped linear launch");
 }
 
+int64_t moe_grouped_bias_grad_bytes(int32_t E, int32_t M, int32_t N) {
+  if (E < 1 || E > kMaxExperts || M < 0 || M > kMaxRows || N < 8 || N % 8 || N > kMaxDim) {
+    fail(MOE_ERR_INVALID_ARG, "E = %d, M = %d, N = %d outside the bias gradient's range", E, M, N);
+    return -1;
+  }
+  return (int64_t)bias_grad_ws_bytes(E, M, N);
+}
+
 moe_status_t moe_grouped_bias_grad(const void* dy, int64_t dy_ld, int32_t dtype, const int32_t* offsets, int32_t E,
-                                   int32_t M, int32_t N, void* db, int64_t db_ld, int32_t out_dtype,
-                                   moe_stream_t stream) {
+                                   int32_t M, int32_t N, void* db, int64_t db_ld, int32_t out_dtype, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream) {
   moe_status_t st = check_groups(dtype, offsets, E, M, N, 8, out_dtype, 8);
   if (st != MOE_OK) return st;
   if ((M > 0 && (st = check_matrix("dy", dy, dy_ld, N)) != MOE_OK) ||
       (st = check_matrix("db", db, db_ld, N)) != MOE_OK)
     return st;
+  const size_t need = bias_grad_ws_bytes(E, M, N);
+  if (need > 0 && (!ws || !aligned(ws, 16)))
+    return fail(MOE_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   BiasGradParams p{};
-  p.dy = dy, p.ld = dy_ld, p.offsets = offsets, p.E = E, p.M = M, p.N = N, p.db = db, p.db_ld = db_ld;
+  p.dy = dy, p.ld = dy_ld, p.offsets = offsets, p.E = E, p.M = M, p.N = N, p.db = db, p.db_ld = db_ld, p.ws = ws;
   const hipStream_t s = (hipStream_t)stream;
   return launched(run("grouped_bias_grad", s, [&] { return launch_bias_grad(p, dtype, out_dtype, s); }),
                   "bias gradient launch");

@@ -17,48 +17,48 @@ namespace {
 
 constexpr int kRowsAhead = 8;   // rows whose loads are in flight together
 
-// A thread sums 8 columns of a token at a time. 1 << lg threads (a power of two,
-// at most 256) lie along a row; where it is longer, `parts` workgroups share it
-// and go through their columns one block of 2048 after another. ROW: a wave's
-// lanes have one token, whose slots and weights are scalars.
+// A thread sums 8 columns of a token. 1 << lg threads (a power of two, at most
+// 256) lie along a row, `parts` workgroups where it is longer. ROW: a wave's
+// lanes have one token, whose slots and weights are scalars. (One workgroup that
+// goes through the parts of its row measured 2.8 -> 6.3 us for a token of 7168,
+// 24 -> 25 for 1024 tokens and 96 -> 98 for 4096.)
 template <int TYPE, bool ROW>
 __global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type, int lg, int parts) {
   const int blk = parts == 1 ? blockIdx.x : blockIdx.x / parts, part = blockIdx.x - blk * parts;
   const int row = threadIdx.x >> lg;
   const int64_t t = (int64_t)blk * (256 >> lg) + (ROW ? __builtin_amdgcn_readfirstlane(row) : row);
-  if (t >= p.T) return;
+  const int col = 8 * (part * 256 + (threadIdx.x & ((1 << lg) - 1)));
+  if (t >= p.T || col >= p.H) return;
   const int32_t* slots = p.slots + t * p.topk;
-  for (int col = 8 * (part * 256 + (threadIdx.x & ((1 << lg) - 1))); col < p.H; col += 2048 * parts) {
-    float acc[8] = {};
-    for (int j0 = 0; j0 < p.topk; j0 += kRowsAhead) {
-      int slot[kRowsAhead];
-      float w[kRowsAhead];
-      Raw8<TYPE> raw[kRowsAhead];
+  float acc[8] = {};
+  for (int j0 = 0; j0 < p.topk; j0 += kRowsAhead) {
+    int slot[kRowsAhead];
+    float w[kRowsAhead];
+    Raw8<TYPE> raw[kRowsAhead];
 #pragma unroll
-      for (int j = 0; j < kRowsAhead; ++j) {
-        const bool in = j0 + j < p.topk;
-        slot[j] = in ? slots[j0 + j] : -1;
-        w[j] = in && p.w ? p.w[t * p.topk + j0 + j] : 1.f;
-      }
-#pragma unroll
-      for (int j = 0; j < kRowsAhead; ++j) {
-        raw[j].zero();
-        if (slot[j] >= 0 && slot[j] < p.R) raw[j].load(p.y, slot[j] * p.y_ld + col);
-      }
-#pragma unroll
-      for (int j = 0; j < kRowsAhead; ++j) {
-        if (slot[j] < 0 || slot[j] >= p.R) continue;
-        float v[8];
-        raw[j].get(v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(w[j], v[k], acc[k]);
-      }
+    for (int j = 0; j < kRowsAhead; ++j) {
+      const bool in = j0 + j < p.topk;
+      slot[j] = in ? slots[j0 + j] : -1;
+      w[j] = in && p.w ? p.w[t * p.topk + j0 + j] : 1.f;
     }
-    const int64_t at = t * p.out_ld + col;
-    if (out_type == TYPE_BF16) store8<TYPE_BF16>(p.out, at, acc);
-    else if (out_type == TYPE_F16) store8<TYPE_F16>(p.out, at, acc);
-    else store8<TYPE_F32>(p.out, at, acc);
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      raw[j].zero();
+      if (slot[j] >= 0 && slot[j] < p.R) raw[j].load(p.y, slot[j] * p.y_ld + col);
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      if (slot[j] < 0 || slot[j] >= p.R) continue;
+      float v[8];
+      raw[j].get(v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(w[j], v[k], acc[k]);
+    }
   }
+  const int64_t at = t * p.out_ld + col;
+  if (out_type == TYPE_BF16) store8<TYPE_BF16>(p.out, at, acc);
+  else if (out_type == TYPE_F16) store8<TYPE_F16>(p.out, at, acc);
+  else store8<TYPE_F32>(p.out, at, acc);
 }
 
 constexpr int kHeld = 4;        // pieces of 8 values of d_out that a thread holds
@@ -74,12 +74,13 @@ __global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, 
   if ((int)blockIdx.x < pad_blocks) {
     const int lo = p.offsets ? max(p.offsets[0], 0) : 0, hi = p.offsets ? min(p.offsets[p.E], p.R) : p.R;
     const float zero[8] = {};
-    for (int i = wave; i < kPadRows; i += 4) {
-      const int64_t r = (int64_t)blockIdx.x * kPadRows + i;
-      if (r < lo || r >= hi) continue;
-      const int src = p.row_src[r];
-      if (src >= 0 && (int64_t)src < (int64_t)p.T * p.topk) continue;
-      for (int c = 8 * lane; c < p.H; c += 512) store8<TYPE, true>(p.d_y, r * p.dy_ld + c, zero);
+    int src[kPadRows / 4];
+    const int64_t r0 = (int64_t)blockIdx.x * kPadRows + wave * (kPadRows / 4);
+#pragma unroll
+    for (int i = 0; i < kPadRows / 4; ++i) src[i] = r0 + i >= lo && r0 + i < hi ? p.row_src[r0 + i] : 0;
+    for (int i = 0; i < kPadRows / 4; ++i) {
+      if (r0 + i < lo || r0 + i >= hi || (src[i] >= 0 && (int64_t)src[i] < (int64_t)p.T * p.topk)) continue;
+      for (int c = 8 * lane; c < p.H; c += 512) store8<TYPE, true>(p.d_y, (r0 + i) * p.dy_ld + c, zero);
     }
     return;
   }
@@ -156,7 +157,7 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
   const int H8 = p.H / 8;
   int lg = 0;
   while (lg < 8 && (1 << lg) < H8) ++lg;
-  const int parts = p.T >= 2048 ? 1 : (H8 + 255) / 256;
+  const int parts = (H8 + 255) / 256;
   const int64_t g = ((int64_t)p.T + (256 >> lg) - 1) / (256 >> lg) * parts;
   if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   auto go = [&](auto ty) {
@@ -171,9 +172,10 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
 }
 
 hipError_t launch_combine_grad(const CombineParams& p, int type, hipStream_t s) {
-  const bool wide = p.H > 1024;
+  const bool wide = p.H > 2048;
   // few tokens: their rows one by one
-  const int parts = p.T >= 1024 ? 1 : p.topk, each = p.T >= 1024 ? p.topk : 1;
+  const bool split = p.T < (wide ? 512 : 4096);
+  const int parts = split ? p.topk : 1, each = split ? 1 : p.topk;
   const int64_t teams = (int64_t)p.T * parts, blocks = wide ? teams : (teams + 3) / 4;
   const int pads = p.row_src ? (p.R + kPadRows - 1) / kPadRows : 0;
   const int64_t g = blocks + pads;
