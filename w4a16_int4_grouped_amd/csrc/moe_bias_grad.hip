@@ -3,7 +3,7 @@
 // A workgroup sums 64 columns of one group: 8 lanes lie along a row (16 bytes
 // each, a line), the others and the waves along the rows, whose sums meet in a
 // fixed order. HBM bounds it where there are enough groups and columns: 24576
-// rows of 4096 in 48 groups 34 us (6.0 TB/s). A workgroup alone reads 88 GB/s:
+// rows of 4096 in 48 groups 34 us (6.0 TB/s). A workgroup alone reads some 60 to 90 GB/s:
 // where groups are few and long, the rows are cut into chunks, a workgroup sums
 // 64 columns of a chunk for each group in it, and a second kernel adds the
 // chunks' sums up. Part c + e of the workspace belongs to chunk c and group e; no
@@ -128,12 +128,19 @@ __global__ __launch_bounds__(64 * kWaves) void bias_grad_finish(BiasGradParams p
 
 int64_t chunks_of(int M) { return ((int64_t)M + kChunk - 1) / kChunk; }
 
-// Whether the rows are cut: an even group's time in one workgroup, and no less
-// than all bytes at 5.5 TB/s, against those bytes and a second kernel's 4 us.
+// Whether the rows are cut: where an even group's rows take one workgroup longer
+// (at 60 GB/s) than all bytes at 5.5 TB/s and a second kernel's 3.5 us. In us,
+// whole / cut (groups, rows in all, columns; the one taken is marked):
+//   1, 2048, 512     5.1 / 4.9*      1, 24576, 64     34 / 5.8*       4, 8192, 1024    8.3* / 6.7
+//   1, 4096, 512     7.8 / 4.9*      1, 24576, 512    73 / 7.8*       8, 24576, 64     9.2 / 5.6*
+//   2, 4096, 7168    12* / 13        1, 24576, 4096   93 / 36*        8, 16384, 4096   25* / 25
+//   16, 8192, 1024   4.2* / 6.7      48, 24576, 4096  37* / 37        8, 448, 4096     3.4* / 9.7
+// The rule takes the rows as even over the groups: where one of many has most of
+// them, it alone takes as long as a single group.
 bool cut(int E, int M, int N) {
-  const double rows = (double)M / E, waves = (double)E * ((N + 63) / 64) / 512, bytes = (double)M * N * 2 / 5.5e6;
-  const double alone = rows * 128 / 88e3 * (waves > 1 ? waves : 1);
-  return (alone > bytes ? alone : bytes) > bytes + 4;
+  const double bytes = (double)M * N * 2 / 5.5e6, waves = (double)E * ((N + 63) / 64) / 512;
+  const double alone = (double)M / E * 128 / 60e3 * (waves > 1 ? waves : 1);
+  return alone > bytes + 3.5;
 }
 
 }  // namespace

@@ -122,7 +122,10 @@ __device__ __forceinline__ void store_codes(int8_t* q, uint8_t* scales, int c, i
 }
 
 constexpr int kQuant = 4, kDequant = 4, kPairs = 2;   // groups per thread (pairs: of both halves)
-constexpr int kRoutedRows = 4;                        // WIDE rows of a workgroup, where they are those of a routing
+// WIDE rows of a workgroup, where they are the many rows of a routing. In us for
+// 1 / 4 rows: 11536 rows of 7168 39 / 37, 35808 112 / 112, 68288 281 / 209, 134064
+// 639 / 518; of 4096 11552 29 / 31, 35664 80 / 79, 68512 160 / 146.
+constexpr int kRoutedRows = 4, kManyRows = 32768;
 
 template <int TYPE, int MODE>
 __global__ __launch_bounds__(256) void mx8_quant(const void* __restrict__ x, int64_t rows, int K8, int64_t ld,
@@ -312,7 +315,7 @@ hipError_t launch_mx8_quant(const void* x, int type, int64_t rows, int K, int64_
 
 hipError_t launch_mx8_dequant(const Mx8Rows& p, int type, hipStream_t s) {
   Shape sh = shape_of(p.out_rows, p.K / 8, kDequant);
-  const bool many = sh.mode == WIDE && p.row_src && sh.blocks >= 4096;
+  const bool many = sh.mode == WIDE && p.row_src && p.out_rows >= kManyRows;
   if (many) sh = shape_of((p.out_rows + kRoutedRows - 1) / kRoutedRows, p.K / 8, kDequant);
   return choose(type, sh, [&](auto ty, auto mode) {
     constexpr int TYPE = decltype(ty)::value, MODE = decltype(mode)::value;

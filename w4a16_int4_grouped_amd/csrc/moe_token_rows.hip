@@ -62,14 +62,26 @@ __global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type
 }
 
 constexpr int kHeld = 4;        // pieces of 8 values of d_out that a thread holds
-
 constexpr int kPadRows = 16;
 
-// TEAM threads (64 or 256) take `each` of a token's rows. The first workgroups
-// look through kPadRows rows each for such as no token names and write 0 there.
+// The sum over a team's lanes, 16 (a row of lanes: rotations by 1, 2, 4 and 8) or 64.
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v) {
+  if constexpr (TEAM == 16) {
+    v += dpp_or_0<0x121>(v);
+    v += dpp_or_0<0x122>(v);
+    v += dpp_or_0<0x124>(v);
+    return v + dpp_or_0<0x128>(v);
+  }
+  return wave_sum_of(v);
+}
+
+// TEAM threads (16, 64 or 256) take `each` of a token's rows, 16 threads only of
+// up to 512 columns. The first workgroups look through kPadRows rows each for
+// such as no token names and write 0 there.
 template <int TYPE, int TEAM>
 __global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, int each, int pad_blocks) {
-  __shared__ float sums[4][64];   // of a wave, per row
+  __shared__ float sums[4][64];   // TEAM 256: of a wave, per row
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if ((int)blockIdx.x < pad_blocks) {
     const int lo = p.offsets ? max(p.offsets[0], 0) : 0, hi = p.offsets ? min(p.offsets[p.E], p.R) : p.R;
@@ -84,12 +96,12 @@ __global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, 
     }
     return;
   }
-  const int block = (int)blockIdx.x - pad_blocks;
-  const int team = TEAM == 64 ? block * 4 + wave : block;
-  const int64_t t = team / parts;
-  const int id = TEAM == 64 ? lane : threadIdx.x;
+  const int64_t block = (int)blockIdx.x - pad_blocks;
+  const int64_t team = TEAM == 16 ? (block * 4 + wave) * 4 + lane / 16 : TEAM == 64 ? block * 4 + wave : block;
+  const int64_t t = parts == 1 ? team : (uint32_t)team / (uint32_t)parts;
+  const int id = TEAM == 16 ? lane % 16 : TEAM == 64 ? lane : threadIdx.x;
+  const int j0 = (int)(team - t * parts) * each, j1 = min(j0 + each, p.topk);
   if (t < p.T) {
-    const int j0 = (team - (int)t * parts) * each, j1 = min(j0 + each, p.topk);
     float mine = 0.f;             // lane j: of row j0 + j, in this wave's columns
     for (int base = 0; base < p.H; base += TEAM * 8 * kHeld) {
       float d[kHeld][8];
@@ -104,10 +116,10 @@ __global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, 
       }
       for (int j = j0; j < j1; ++j) {
         const int slot = p.slots[t * p.topk + j];
-        if (slot < 0 || slot >= p.R) continue;
+        const bool has = slot >= 0 && slot < p.R;
         const float w = p.w ? p.w[t * p.topk + j] : 1.f;
         float dot = 0.f;
-        if (p.y) {
+        if (has && p.y) {
           Raw8<TYPE> raw[kHeld];
 #pragma unroll
           for (int i = 0; i < kHeld; ++i) {
@@ -122,29 +134,31 @@ __global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, 
             for (int k = 0; k < 8; ++k) dot = __builtin_fmaf(d[i][k], v[k], dot);
           }
         }
+        if (has) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          if (cols[i] >= p.H) continue;
-          float v[8];
+          for (int i = 0; i < kHeld; ++i) {
+            if (cols[i] >= p.H) continue;
+            float v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = w * d[i][k];
-          store8<TYPE, true>(p.d_y, slot * p.dy_ld + cols[i], v);
+            for (int k = 0; k < 8; ++k) v[k] = w * d[i][k];
+            store8<TYPE, true>(p.d_y, slot * p.dy_ld + cols[i], v);
+          }
         }
-        if (p.y) {
-          const float sum = wave_sum_of(dot);
-          if (lane == j - j0) mine += sum;
+        if (p.d_w) {
+          const float sum = team_sum<TEAM>(dot);
+          if (TEAM == 16) {
+            if (id == 0) p.d_w[t * p.topk + j] = sum;
+          } else if (lane == j - j0) {
+            mine += sum;
+          }
         }
       }
     }
-    if (TEAM == 64) {
-      if (p.d_w && lane < j1 - j0) p.d_w[t * p.topk + j0 + lane] = mine;
-    } else {
-      sums[wave][lane] = mine;
-    }
+    if (TEAM == 64 && p.d_w && lane < j1 - j0) p.d_w[t * p.topk + j0 + lane] = mine;
+    if (TEAM == 256) sums[wave][lane] = mine;
   }
   if (TEAM == 256) {              // t < T for all of the workgroup, or for none
     __syncthreads();
-    const int j0 = (team - (int)t * parts) * each, j1 = min(j0 + each, p.topk);
     if (t < p.T && p.d_w && threadIdx.x < (unsigned)(j1 - j0))
       p.d_w[t * p.topk + j0 + threadIdx.x] =
           sums[0][threadIdx.x] + sums[1][threadIdx.x] + sums[2][threadIdx.x] + sums[3][threadIdx.x];
@@ -171,20 +185,49 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
   return hipGetLastError();
 }
 
+// Threads of a team, and whether it takes a token's rows one by one. Measured in
+// us (BF16, top-8, 384 experts with groups padded to 16 rows; 64 and 256 threads,
+// all rows / one row a team; the form taken is marked):
+//   columns, tokens     64: all    one   256: all    one
+//    7168      16           54     12         18    6.1*
+//    7168     128           78     28         32     28*
+//    7168     512           84     39*        39     41
+//    7168    1024          101     75         64*    76
+//    7168    4096          234    229        216*   267
+//    2880      16           23    6.2         12    4.8*
+//    2880     512           38     18*        24     20
+//    2880    1024           45     31         30*    34
+//    2880    4096           96     91         91*   109
+//    2048     512           22     12*        18     16
+//    2048    2048           35     36*        39     46
+//    1536    4096           49*    48         54     76
+// 48 experts:
+//    1024    8192           68*    64         86    132
+//    2048   16384          234*   241        229    316
+namespace {
+struct Team {
+  int threads;
+  bool one;
+};
+Team team_of(int T, int H) {
+  if (H > 2048) return T <= 128 ? Team{256, true} : T < 1024 ? Team{64, true} : Team{256, false};
+  return Team{H > 512 ? 64 : 16, T < 4096};
+}
+}  // namespace
+
 hipError_t launch_combine_grad(const CombineParams& p, int type, hipStream_t s) {
-  const bool wide = p.H > 2048;
-  // few tokens: their rows one by one
-  const bool split = p.T < (wide ? 512 : 4096);
-  const int parts = split ? p.topk : 1, each = split ? 1 : p.topk;
-  const int64_t teams = (int64_t)p.T * parts, blocks = wide ? teams : (teams + 3) / 4;
+  const Team m = team_of(p.T, p.H);
+  const int parts = m.one ? p.topk : 1, each = m.one ? 1 : p.topk;
+  const int64_t teams = (int64_t)p.T * parts, blocks = (teams * m.threads + 255) / 256;
   const int pads = p.row_src ? (p.R + kPadRows - 1) / kPadRows : 0;
   const int64_t g = blocks + pads;
   if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   if (g == 0) return hipSuccess;
   auto go = [&](auto ty) {
     constexpr int TYPE = decltype(ty)::value;
-    if (wide) combine_grad<TYPE, 256><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
-    else combine_grad<TYPE, 64><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
+    if (m.threads == 256) combine_grad<TYPE, 256><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
+    else if (m.threads == 64) combine_grad<TYPE, 64><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
+    else combine_grad<TYPE, 16><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
   };
   if (type == TYPE_BF16) go(std::integral_constant<int, TYPE_BF16>{});
   else if (type == TYPE_F16) go(std::integral_constant<int, TYPE_F16>{});
