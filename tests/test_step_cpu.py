@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import w4a16_int4_grouped_amd as M
-from tests.test_operators_cpu import ODD, OK, L, refused  # noqa: F401
+from tests.test_operators_cpu import BAD_GEMM, ODD, OK, L, refused  # noqa: F401
 from tests.test_operators_streams_cpu import CALLER, OTHER, Made, Stream
 from tests.test_operators_views_cpu import Standin
 
@@ -158,6 +158,46 @@ def test_swiglu_gradient_refusals(L, kw, word):  # noqa: F811
     refused(L.moe_swiglu_grad(*dict(GRAD, **kw).values(), None), word)
 
 
+LINEAR = dict(a=OK, a_ld=64, w=OK, w_stride=64 * 64, w_ld=64, dtype=0, offsets=OK, E=4, M=16, N=64, K=64, bias=OK,
+              bias_dtype=0, bias_ld=64, act=0, residual=OK, res_ld=64, out=OK, out_ld=64, out_dtype=0)
+
+
+@pytest.mark.parametrize("kw,word", BAD_GEMM + [
+    (dict(bias=ODD), "bias"), (dict(bias_ld=56), "bias"), (dict(bias_ld=68), "bias"), (dict(bias_dtype=3), "bias_dtype"),
+    (dict(act=2), "act"), (dict(act=-1), "act"), (dict(act=1, N=56, w_stride=0), "N = 56"), (dict(residual=ODD), "residual"),
+    (dict(res_ld=56), "residual"), (dict(act=1, out_ld=24), "out"), (dict(act=1, res_ld=24), "residual"),
+])
+def test_linear_refusals(L, kw, word):  # noqa: F811
+    refused(L.moe_grouped_linear(*dict(LINEAR, **kw).values(), None), word)
+
+
+BIAS = dict(dy=OK, dy_ld=64, dtype=0, offsets=OK, E=4, M=16, N=64, db=OK, db_ld=64, out_dtype=2, ws=OK, ws_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(dy=None), "dy"), (dict(dy=ODD), "dy"), (dict(dy_ld=56), "dy"), (dict(dtype=2), "BF16 or FP16"),
+    (dict(offsets=None), "offsets"), (dict(E=0), "E ="), (dict(M=-1), "M ="), (dict(N=60), "multiples"), (dict(N=0), "N ="),
+    (dict(db=None), "db"), (dict(db_ld=60), "db"), (dict(out_dtype=3), "out_dtype"),
+    (dict(E=1, M=24576, ws=None), "workspace"), (dict(E=1, M=24576, ws=ODD), "workspace"),
+])
+def test_bias_gradient_refusals(L, kw, word):  # noqa: F811
+    refused(L.moe_grouped_bias_grad(*dict(BIAS, **kw).values(), None), word)
+
+
+def test_bias_gradient_workspace(L):  # noqa: F811
+    size = L.moe_grouped_bias_grad_bytes
+    for E, M_, N in ((48, 24576, 4096), (8, 448, 4096), (16, 8192, 1024), (2, 4096, 7168), (1, 0, 64), (4096, 1 << 30, 8)):
+        assert size(E, M_, N) == 0 or M_ == 1 << 30
+    for E, M_, N in ((1, 24576, 64), (1, 24576, 4096), (8, 24576, 64), (1, 4096, 512)):
+        # a part for each chunk of 256 rows, and for each group one more
+        assert size(E, M_, N) == (M_ // 256 + E) * N * 4
+    need = size(1, 24576, 64)
+    status = L.moe_grouped_bias_grad(*dict(BIAS, E=1, M=24576, ws_bytes=need - 1).values(), None)
+    assert status == M.MOE_ERR_WORKSPACE_TOO_SMALL and str(need) in M.last_error()
+    for bad in ((0, 1, 8), (4097, 1, 8), (1, -1, 8), (1, (1 << 30) + 1, 8), (1, 1, 4), (1, 1, (1 << 20) + 8)):
+        assert size(*bad) == -1
+
+
 # ---- the binding ----------------------------------------------------------------------
 
 
@@ -176,6 +216,9 @@ CALLS = {
     "mx8_dequant": lambda s=None: M.mx8_dequant(T(40, 64, dtype=Q), T(40, 16, dtype=U), row_src=T(80, dtype=I), topk=2,
                                                 stream=s),
     "swiglu_save": lambda s=None: M.swiglu_save(T(40, 64), offsets=T(3, dtype=I), stream=s),
+    "grouped_linear": lambda s=None: M.grouped_linear(T(40, 64), T(3, 32, 64), T(4, dtype=I), bias=T(3, 32), act="swiglu",
+                                                      residual=T(40, 16), stream=s),
+    "grouped_bias_grad": lambda s=None: M.grouped_bias_grad(T(40, 64), T(4, dtype=I), stream=s),
     "swiglu_grad": lambda s=None: M.swiglu_grad(T(40, 2, 32, dtype=Q), T(40, 32), scales=T(40, 2, 16, dtype=U), stream=s),
 }
 
@@ -189,8 +232,8 @@ class Lib:
     def __getattr__(self, f):
         if f.endswith("scale_cols"):
             return lambda K: ((K + 31) // 32 + 15) // 16 * 16
-        if f.endswith("balance_bytes"):
-            return lambda T, E, S: 4096
+        if f.endswith("balance_bytes") or f.endswith("bias_grad_bytes"):
+            return lambda *sizes: 4096
         return lambda *args: self.launched.append((f, args)) or M.MOE_OK
 
 
@@ -199,13 +242,17 @@ def fake(monkeypatch):
     M._load()
     fake_lib = Lib()
     monkeypatch.setattr(M, "_lib", fake_lib)
+    monkeypatch.setattr(M, "lib", lambda: fake_lib)
     monkeypatch.setattr(M, "_new", lambda shape, dtype, device, stream: Standin(shape, dtype))
     monkeypatch.setattr(Standin, "device", torch.device("cuda", 0))
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
-    M.mx8_scale_cols.cache_clear()
+    caches = (M.mx8_scale_cols, M._balance_bytes, M._bias_grad_bytes)
+    for c in caches:
+        c.cache_clear()
     yield fake_lib.launched
-    M.mx8_scale_cols.cache_clear()
+    for c in caches:
+        c.cache_clear()
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -250,6 +297,16 @@ BAD = [
     ("dequant: out of another height", lambda: M.mx8_dequant(T(40, 64, dtype=Q), T(40, 16, dtype=U), row_src=T(80, dtype=I),
                                                              out=T(40, 64))),
     ("dequant: topk", lambda: M.mx8_dequant(T(40, 64, dtype=Q), T(40, 16, dtype=U), row_src=T(80, dtype=I), topk=0)),
+    ("linear: act", lambda: M.grouped_linear(T(40, 64), T(3, 32, 64), T(4, dtype=I), act="gelu")),
+    ("linear: bias of another width", lambda: M.grouped_linear(T(40, 64), T(3, 32, 64), T(4, dtype=I), bias=T(3, 16), act="swiglu")),
+    ("linear: bias of another type", lambda: M.grouped_linear(T(40, 64), T(3, 32, 64), T(4, dtype=I), bias=T(3, 32, dtype=I))),
+    ("linear: residual of another type", lambda: M.grouped_linear(T(40, 64), T(3, 32, 64), T(4, dtype=I), residual=T(40, 32, dtype=F))),
+    ("linear: residual of another width", lambda: M.grouped_linear(T(40, 64), T(3, 32, 64), T(4, dtype=I), residual=T(40, 32), act="swiglu")),
+    ("linear: out of another width", lambda: M.grouped_linear(T(40, 64), T(3, 32, 64), T(4, dtype=I), out=T(40, 32), act="swiglu")),
+    ("linear: columns", lambda: M.grouped_linear(T(40, 72), T(3, 32, 64), T(4, dtype=I))),
+    ("bias gradient: no offsets", lambda: M.grouped_bias_grad(T(40, 64), None)),
+    ("bias gradient: out of another height", lambda: M.grouped_bias_grad(T(40, 64), T(4, dtype=I), out=T(4, 64))),
+    ("bias gradient: workspace", lambda: M.grouped_bias_grad(T(40, 64), T(4, dtype=I), ws=T(9999, dtype=F))),
     ("save: odd width", lambda: M.swiglu_save(T(40, 63))),
     ("save: codes in two dimensions", lambda: M.swiglu_save(T(40, 64), out=(T(40, 32), T(40, 64, dtype=Q), T(40, 2, 16, dtype=U)))),
     ("gradient: h of another type", lambda: M.swiglu_grad(T(40, 64, dtype=H16), T(40, 32))),
@@ -299,7 +356,10 @@ def test_outputs_come_from_the_launch_streams_memory(monkeypatch):
     monkeypatch.setattr(M, "_torch", stand_in)
     monkeypatch.setattr(M, "_call", lambda fn, device, stream, *args: None)
     monkeypatch.setattr(M, "_lib", Lib())
-    M.mx8_scale_cols.cache_clear()
+    monkeypatch.setattr(M, "lib", lambda: M._lib)
+    caches = (M.mx8_scale_cols, M._balance_bytes, M._bias_grad_bytes)
+    for c in caches:
+        c.cache_clear()
     for name, call in CALLS.items():
         outputs.clear()
         call(OTHER)
@@ -307,4 +367,5 @@ def test_outputs_come_from_the_launch_streams_memory(monkeypatch):
         outputs.clear()
         call(None)
         assert outputs and all(t.made_on is CALLER and not t.kept_for for t in outputs), name
-    M.mx8_scale_cols.cache_clear()
+    for c in caches:
+        c.cache_clear()

@@ -204,6 +204,12 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
 // 48 experts:
 //    1024    8192           68*    64         86    132
 //    2048   16384          234*   241        229    316
+// 48 experts, 16 and 64 threads:   16: all    one    64: all    one
+//      64    2048                     7.2    4.2*       7.9    7.7
+//      64   16384                      22     25*        40     55
+//     256    2048                      11    6.7*        14     11
+//     512    2048                      16    9.7*        17     13
+//     512   16384                      65     59*        66     80
 namespace {
 struct Team {
   int threads;
@@ -211,7 +217,7 @@ struct Team {
 };
 Team team_of(int T, int H) {
   if (H > 2048) return T <= 128 ? Team{256, true} : T < 1024 ? Team{64, true} : Team{256, false};
-  return Team{H > 512 ? 64 : 16, T < 4096};
+  return H > 512 ? Team{64, T < 4096} : Team{16, true};
 }
 }  // namespace
 
