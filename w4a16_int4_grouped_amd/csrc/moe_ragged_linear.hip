@@ -3,7 +3,8 @@
 //
 // The tiles are those of the plain product (moe_ragged_tile.h). For SwiGLU a
 // tile's rows of weights alternate, 32 gate rows and the 32 up rows that belong
-// to them, so that a lane holds both values of a pair.
+// to them (16 and 16 where the tile has 32), so that a lane holds both values of
+// a pair.
 #include "moe_ragged_tile.h"
 
 namespace moe {

@@ -196,8 +196,9 @@ __device__ __forceinline__ void fence() {
 // conflict in every second cycle).
 __device__ __forceinline__ int spread(int r) { return ((r >> 1) & 3) | (((r >> 4) & 1) << 2); }
 
-// GLU (not COL): of 64 rows the first 32 are gate rows of the weights, the
-// others the up rows that belong to them, from `far` bytes on.
+// GLU (not COL): of 64 rows (32 where the tile has no more) the first half are
+// gate rows of the weights, the others the up rows that belong to them, `far`
+// bytes behind.
 template <int FMT, bool COL, int B, int NW, bool GLU = false>
 struct Operand {
   static constexpr int kBytes = B * kStageBytes;
@@ -208,7 +209,8 @@ struct Operand {
   __device__ __forceinline__ static int chunk_swizzle(int r) { return B >= 128 ? 2 * (r & 3) : B == 64 ? r & 2 : 0; }
   static constexpr int kTiles = 4;                 // fragments a wave may hold
   static_assert(B / 8 % NW == 0 && kRowB <= 1024, "whole copies");
-  static_assert(!GLU || (!COL && B % 64 == 0 && (NW == 1 || NW == 4 || NW == 8)), "whole pairs of 32 rows");
+  static_assert(!GLU || (!COL && (B % 64 == 0 ? NW == 1 || NW == 4 || NW == 8 : B == 32 && NW == 1)),
+                "pairs of 32 or 16 rows in whole copies");
   // not COL: spread() of a copy's rows changes with 16 rows, so with the copy where fewer than 4 waves share them
   static constexpr int kVar = COL || NW >= 4 ? 1 : 2;
   static constexpr int variant(int i) { return kVar == 1 ? 0 : NW == 2 ? i & 1 : (i >> 1) & 1; }
@@ -276,8 +278,9 @@ struct Operand {
     for (int i = 0; i < kCopies; ++i) {
       if (i < from || i >= to) continue;
       if constexpr (GLU) {   // rows 8 (i NW + wave) .. + 7 of the tile
-        const int r8 = i * NW + wave, half = NW == 4 ? i & 1 : NW == 8 ? wave >> 2 : (i >> 2) & 1;
-        const int row = (r8 >> 3) * 32 + (r8 & 3) * 8;
+        const int r8 = i * NW + wave;
+        const int half = B == 32 ? i >> 1 : NW == 4 ? i & 1 : NW == 8 ? wave >> 2 : (i >> 2) & 1;
+        const int row = B == 32 ? (i & 1) * 8 : (r8 >> 3) * 32 + (r8 & 3) * 8;
         copy16(stage + r8 * 1024, half ? up : r, v[variant(i)], row * (int)ld + at);
       } else {
         copy16(stage + (i * NW + wave) * 1024, r, v[variant(i)], i * NW * kRows * (int)ld + at);
@@ -820,7 +823,6 @@ struct SplitBody {
   static constexpr bool MX = FMT == FMT_MX, GLU = EPI == EPI_GLU;
   static constexpr int kVal = MX ? 256 : 64;
   static constexpr int BO = GLU ? BI / 2 : BI;                     // output columns
-  static_assert(!GLU || BI == 64, "32 gate rows and the 32 up rows that belong to them");
   using OpP = Operand<FMT, PC, BI, 1, GLU>;
   using OpQ = Operand<FMT, QC, BJ, 1>;
   static constexpr int kSB = MX ? 2048 : 0;                        // 16 scales of up to 64 rows of each operand
@@ -933,7 +935,7 @@ struct SplitBody {
         f32x4_t up = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < W; ++w)
-          up += *reinterpret_cast<const f32x4_t*>(all + w * (kLds / W) + j * kPitch + (32 + i) * 4);
+          up += *reinterpret_cast<const f32x4_t*>(all + w * (kLds / W) + j * kPitch + (BI / 2 + i) * 4);
         up += bias[1];
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = swiglu(v[k], up[k]);
@@ -979,8 +981,7 @@ hipError_t launch(RaggedParams p, hipStream_t s) {
   constexpr bool GLU = EPI == EPI_GLU;
   if (!QC && p.M == 0) return hipSuccess;
   const int64_t size = p.out_type == TYPE_F32 ? 4 : 2;
-  Form f = form_of(FormCall{FMT == FMT_MX, QC, p.E, p.M, GLU ? 2 * p.I : p.I, p.J, p.C, (int)size});
-  if (GLU && f == THIN) f = SPLIT;   // 32 rows of weights are no gate | up pairs
+  const Form f = form_of(FormCall{FMT == FMT_MX, QC, p.E, p.M, GLU ? 2 * p.I : p.I, p.J, p.C, (int)size});
   const int64_t bytes = (QC ? (int64_t)p.E * p.J : p.M) * p.I * size;
   // Whole lines that the L2s (32 MB) cannot hold leave them to the operands when they pass them by: FP4, 8 experts of
   // 2048 rows 230 against 252 us. FOUR's calls are bound by such writes, and up to 256 MB the last-level cache takes
@@ -995,8 +996,8 @@ hipError_t launch(RaggedParams p, hipStream_t s) {
   if (f == LARGE) ragged_gemm<FMT, PC, QC, 256, 256, 4, 2, false, EPI><<<n, 512, 0, s>>>(p);
   else if (f == TWO) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, false, EPI><<<n, 256, 0, s>>>(p);
   else if (f == FOUR) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, true, EPI><<<n, 256, 0, s>>>(p);
-  else if (GLU || f == SPLIT) ragged_split<FMT, PC, QC, 64, EPI><<<n, 64 * kSplitWaves<FMT, 64>, 0, s>>>(p);
-  else if constexpr (!GLU) ragged_split<FMT, PC, QC, 32, EPI><<<n, 64 * kSplitWaves<FMT, 32>, 0, s>>>(p);
+  else if (f == SPLIT) ragged_split<FMT, PC, QC, 64, EPI><<<n, 64 * kSplitWaves<FMT, 64>, 0, s>>>(p);
+  else ragged_split<FMT, PC, QC, 32, EPI><<<n, 64 * kSplitWaves<FMT, 32>, 0, s>>>(p);
   return hipGetLastError();
 }
 
