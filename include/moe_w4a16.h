@@ -563,8 +563,8 @@ moe_status_t moe_grouped_bias_grad(const void* dy, int64_t dy_ld, int32_t dtype,
  * every time. */
 
 /* Bytes of moe_router_balance's workspace for T tokens, E experts and S
- * sequences (limits there), 0 for others. */
-size_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S);
+ * sequences: 0 where it needs none, -1 for sizes outside its limits. */
+int64_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S);
 
 /* Rows per expert and the load-balance loss of each sequence of tokens.
  * Sequence s holds the n rows [offsets[s], offsets[s + 1]) (device int32
@@ -579,8 +579,8 @@ size_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S);
  *   logits    device [T, E] of dtype, rows ld values apart (any alignment of
  *             the type); topk_ids device int32 [T, topk]
  *   loss      device float [S], counts device int32 [S, E], fully written
- *   ws        device, 16-byte aligned, of ws_bytes >= moe_router_balance_bytes;
- *             nothing in it has to be kept or cleared between calls
+ *   ws        device, 16-byte aligned, of ws_bytes >= moe_router_balance_bytes
+ *             (NULL if that is 0); nothing in it has to be kept or cleared
  * T 0..2^24, E 1..4096, topk 1..min(E, 64), S 1..2^20, S * E up to 2^30.
  * Enqueues up to two kernels. Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, HIP. */
 moe_status_t moe_router_balance(const void* logits, int32_t dtype, int64_t ld, int32_t T,

@@ -50,6 +50,9 @@ def loss_close(got, want, logits, T):
     (1, 1, 1, None, "softmax", "fp32", False),
     (1, 384, 8, None, "sigmoid", "bf16", False),
     (32, 8, 2, None, "softmax", "fp32", True),
+    (64, 20, 3, [5, 61], "sigmoid", "bf16", True),
+    (50, 20, 3, [7, 7], "softmax", "fp32", False),
+    (65, 20, 3, None, "softmax", "fp16", False),
     (33, 64, 6, None, "sigmoid", "fp16", True),
     (31, 65, 3, [0, 31], "softmax", "bf16", True),
     (300, 100, 4, [0, 0, 1, 1, 33, 200, 300, 300], "sigmoid", "fp32", True),

@@ -141,7 +141,7 @@ def lib() -> ctypes.CDLL:
         "moe_mx_quant": (S, [P, I32, I64, I64, I32, P, P, P]),
         "moe_mx_dequant": (S, [P, P, I64, I32, P, I32, I64, P]),
         "moe_mx_grouped_gemm": (S, [P, P, P, P, P, I32, I32, I32, I32, P, I64, I32, P]),
-        "moe_router_balance_bytes": (SZ, [I32, I32, I32]),
+        "moe_router_balance_bytes": (I64, [I32, I32, I32]),
         "moe_router_balance": (S, [P, I32, I64, I32, I32, P, I32, I32, P, I32, P, P, P, SZ, P]),
         "moe_router_balance_grad": (S, [P, I32, I64, I32, I32, I32, I32, P, I32, P, P, P, I64, P, I64, P]),
         "moe_combine": (S, [P, I32, I64, I32, I32, P, I32, I32, P, P, I64, I32, P]),
@@ -814,7 +814,7 @@ def _offsets(t, device):
 @functools.lru_cache(maxsize=256)
 def _balance_bytes(T, E, S) -> int:
     n = lib().moe_router_balance_bytes(T, E, S)
-    if n == 0:
+    if n < 0:
         check(MOE_ERR_INVALID_ARG)
     return n
 
@@ -837,7 +837,6 @@ def router_balance(logits, ids, score="softmax", offsets=None, out=None, ws=None
     _fits(T | E | topk)
     _dense(ids, "ids", torch.int32, dev, (T, topk))
     off, S = (None, 1) if offsets is None else _offsets(offsets, dev)
-    L = _lib or lib()
     if out is None:
         loss = _new((S,), torch.float32, dev, stream)
         counts = _new((S, E), torch.int32, dev, stream)
@@ -845,15 +844,15 @@ def router_balance(logits, ids, score="softmax", offsets=None, out=None, ws=None
         loss, counts = out
         _dense(loss, "loss", torch.float32, dev, (S,))
         _dense(counts, "counts", torch.int32, dev, (S, E))
-    if ws is None:
-        nbytes = _balance_bytes(T, E, S)
-        ws = _empty(nbytes, dev, stream)
-    else:
+    nbytes = _balance_bytes(T, E, S)
+    if ws is not None:
         nbytes = ws.numel()
         _dense(ws, "ws", torch.uint8, dev, (nbytes,))
-    _call(L.moe_router_balance, dev, stream,
+    elif nbytes:
+        ws = _empty(nbytes, dev, stream)
+    _call((_lib or lib()).moe_router_balance, dev, stream,
           logits.data_ptr(), _dtype(logits.dtype), ld, T, E, ids.data_ptr(), topk, _score(score), off, S,
-          loss.data_ptr(), counts.data_ptr(), ws.data_ptr(), nbytes)
+          loss.data_ptr(), counts.data_ptr(), None if ws is None else ws.data_ptr(), nbytes)
     return loss, counts
 
 

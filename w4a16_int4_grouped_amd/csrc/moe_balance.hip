@@ -29,8 +29,9 @@ constexpr int kSolo = 64;
 // 24.1; 262144 of 64 (FP32), at most 512 / 1024 / 2048 chunks: 38.1 / 35.2 / 37.4.
 // One sequence of up to kSolo rows is one workgroup's: 64 tokens 6.2 against 7.1
 // us, 128 tokens 10.3 against 7.6.
-int chunk_rows(int T, int E, bool one) {
-  if (one && T <= kSolo) return kSolo;
+bool is_solo(int T, int S) { return S == 1 && T <= kSolo; }
+int chunk_rows(int T, int E, int S) {
+  if (is_solo(T, S)) return kSolo;
   const int least = 4 * kSumWaves, most = E > 64 ? 512 : 1024;
   const int n = (T + most - 1) / most;
   return n > least ? (n + least - 1) / least * least : least;
@@ -46,7 +47,7 @@ __host__ __device__ __forceinline__ int64_t up256(int64_t n) { return (n + 255) 
 
 BalanceWs ws_of(int T, int E, int S) {
   BalanceWs w;
-  w.chunk = chunk_rows(T, E, S == 1);
+  w.chunk = chunk_rows(T, E, S);
   w.chunks = (int)(((int64_t)T + w.chunk - 1) / w.chunk);
   w.groups = (E + 63) / 64;
   const int64_t part = up256(((int64_t)w.chunks + S) * E * 4);
@@ -248,8 +249,8 @@ __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceW
       if (threadIdx.x == 0) {
         double loss = 0.0;
         for (int w = 0; w < W; ++w) loss += shares[w];
-        const double n = p.T;
-        p.loss[0] = p.T > 0 ? (float)(loss * p.E / (n * n * p.topk)) : 0.f;
+        const double n = q.hi - q.lo;
+        p.loss[0] = n > 0 ? (float)(loss * p.E / (n * n * p.topk)) : 0.f;
       }
       return;
     } else {
@@ -433,11 +434,11 @@ hipError_t by_type(int type, F&& f) {
 
 }  // namespace
 
-size_t balance_ws_bytes(int T, int E, int S) { return (size_t)ws_of(T, E, S).bytes; }
+size_t balance_ws_bytes(int T, int E, int S) { return is_solo(T, S) ? 0 : (size_t)ws_of(T, E, S).bytes; }
 
 hipError_t launch_balance(const BalanceParams& p, int type, hipStream_t s) {
   const BalanceWs ws = ws_of(p.T, p.E, p.S);
-  const bool solo = ws.chunks <= 1 && !p.offsets;
+  const bool solo = is_solo(p.T, p.S);
   const hipError_t e = by_type(type, [&](auto ty) {
     return by_experts(p.E, pairs(p.logits, p.ld, type), [&](auto vpl, auto v) {
       return sums_for<decltype(ty)::value, decltype(vpl)::value, decltype(v)::value>(p, ws, solo, s);

@@ -67,13 +67,13 @@ moe_status_t check_swiglu(int dtype, int rows, int I, const int32_t* offsets, in
 
 extern "C" {
 
-size_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S) {
+int64_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S) {
   if (T < 0 || T > kMaxRows / kMaxTopk || E < 1 || E > kMaxExperts || S < 1 || S > kMaxSequences ||
       (int64_t)S * E > kMaxCounts) {
     fail(MOE_ERR_INVALID_ARG, "T = %d, E = %d, S = %d outside the balance loss's range", T, E, S);
-    return 0;
+    return -1;
   }
-  return balance_ws_bytes(T, E, S);
+  return (int64_t)balance_ws_bytes(T, E, S);
 }
 
 moe_status_t moe_router_balance(const void* logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
@@ -84,8 +84,9 @@ moe_status_t moe_router_balance(const void* logits, int32_t dtype, int64_t ld, i
   if (st != MOE_OK) return st;
   if ((T > 0 && !topk_ids) || !loss || !counts || !aligned(topk_ids, 4) || !aligned(loss, 4) || !aligned(counts, 4))
     return fail(MOE_ERR_INVALID_ARG, "topk_ids / loss / counts NULL or misaligned");
-  if (!ws || !aligned(ws, 16)) return fail(MOE_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
   const size_t need = balance_ws_bytes(T, E, S);
+  if (need > 0 && (!ws || !aligned(ws, 16)))
+    return fail(MOE_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
   if (ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   BalanceParams p{};
