@@ -63,6 +63,9 @@ def loss_close(got, want, logits, T):
     (129, 1000, 64, None, "sigmoid", "fp16", True),
     (70, 1024, 7, [0, 70], "softmax", "bf16", False),
     (50, 4096, 33, [0, 7, 50], "softmax", "fp32", True),
+    (16, 2000, 9, None, "softmax", "bf16", True),
+    (31, 700, 9, None, "sigmoid", "fp32", True),
+    (700, 1500, 9, [3, 9, 9, 400, 690], "softmax", "bf16", True),
     (40, 1026, 8, None, "sigmoid", "bf16", False),
     (40000, 16, 2, [0, 39999, 40000], "softmax", "bf16", False),
 ])

@@ -40,7 +40,8 @@ def test_balance_workspace(L):  # noqa: F811
     assert status == M.MOE_ERR_WORKSPACE_TOO_SMALL and str(need) in M.last_error()
     for bad in ((-1, 64, 1), (1 << 25, 64, 1), (4, 0, 1), (4, 4097, 1), (4, 64, 0), (4, 4096, 1 << 19)):
         assert L.moe_router_balance_bytes(*bad) == -1
-    assert L.moe_router_balance_bytes(64, 4096, 1) == 0 < L.moe_router_balance_bytes(65, 8, 1)
+    for E, alone in ((8, 64), (512, 64), (513, 32), (1024, 32), (1025, 16), (4096, 16)):     # rows that need no workspace
+        assert L.moe_router_balance_bytes(alone, E, 1) == 0 < L.moe_router_balance_bytes(alone + 1, E, 1)
     # of the largest calls: parts of 1024 chunks and each sequence
     assert L.moe_router_balance_bytes(1 << 24, 4096, 1) < 1 << 26
 

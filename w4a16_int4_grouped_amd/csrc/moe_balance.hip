@@ -21,18 +21,26 @@ namespace moe {
 namespace {
 
 constexpr int kSumWaves = 8;       // of a workgroup that sums
-constexpr int kSolo = 64;
-
-// Rows of a chunk: 4 a wave, more where there would be too many chunks. In us
-// for both kernels (BF16), chunks of 32 / 64 / 128 rows: 8192 tokens of 384
-// experts 9.7 / 10.7 / 15.3, 16411 of them 13.5 / 11.7 / 14.7, 65536 26.0 / 25.8 /
-// 24.1; 262144 of 64 (FP32), at most 512 / 1024 / 2048 chunks: 38.1 / 35.2 / 37.4.
-// One sequence of up to kSolo rows is one workgroup's: 64 tokens 6.2 against 7.1
-// us, 128 tokens 10.3 against 7.6.
-bool is_solo(int T, int S) { return S == 1 && T <= kSolo; }
+// Rows of a chunk: those whose loads a workgroup has in flight together (more
+// than 1024 experts: twice as many), more where there would be too many chunks.
+// In us for both kernels (BF16), chunks of 8 / 16 / 32 / 64 rows:
+//   experts, tokens    384, 512        8.6    7.9    8.1*   9.7
+//                      384, 4096        12    9.2    8.5*    11
+//                     1024, 512        9.1    8.7*    10     14
+//                     1024, 4096        13     10*    11     16
+//                     4096, 512         15*    18     26     43
+//                     4096, 4096        22*    23     30     47
+// and in chunks of 32 / 64 / 128 rows for 384 experts 16411 tokens 13.5 / 11.7* /
+// 14.7, 65536 tokens 26.0 / 25.8 / 24.1*; for 64 experts 262144 tokens (FP32) in at
+// most 512 / 1024 / 2048 chunks 38.1 / 35.2* / 37.4.
+// One sequence of up to twice as many rows is one workgroup's: 384 experts, 64
+// tokens 6.0 against 7.8 us; 1024, 32 tokens 6.2 against 8.1, 64 tokens 10.3 against
+// 7.9; 4096, 16 tokens 12.8 against 12.6.
+int least_rows(int E) { return E <= 512 ? 32 : E <= 1024 ? 16 : 8; }
+bool is_solo(int T, int E, int S) { return S == 1 && T <= 2 * least_rows(E); }
 int chunk_rows(int T, int E, int S) {
-  if (is_solo(T, S)) return kSolo;
-  const int least = 4 * kSumWaves, most = E > 64 ? 512 : 1024;
+  const int least = least_rows(E), most = E > 64 ? 512 : 1024;
+  if (is_solo(T, E, S)) return 2 * least;
   const int n = (T + most - 1) / most;
   return n > least ? (n + least - 1) / least * least : least;
 }
@@ -434,11 +442,11 @@ hipError_t by_type(int type, F&& f) {
 
 }  // namespace
 
-size_t balance_ws_bytes(int T, int E, int S) { return is_solo(T, S) ? 0 : (size_t)ws_of(T, E, S).bytes; }
+size_t balance_ws_bytes(int T, int E, int S) { return is_solo(T, E, S) ? 0 : (size_t)ws_of(T, E, S).bytes; }
 
 hipError_t launch_balance(const BalanceParams& p, int type, hipStream_t s) {
   const BalanceWs ws = ws_of(p.T, p.E, p.S);
-  const bool solo = is_solo(p.T, p.S);
+  const bool solo = is_solo(p.T, p.E, p.S);
   const hipError_t e = by_type(type, [&](auto ty) {
     return by_experts(p.E, pairs(p.logits, p.ld, type), [&](auto vpl, auto v) {
       return sums_for<decltype(ty)::value, decltype(vpl)::value, decltype(v)::value>(p, ws, solo, s);
