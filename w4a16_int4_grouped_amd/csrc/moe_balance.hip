@@ -14,6 +14,12 @@
 // where one workgroup has all rows). A workgroup's rows are a chunk of all rows,
 // whatever sequences meet in it: part c + s belongs to chunk c and sequence s,
 // no two such pairs have the same sum, because both only grow along the rows.
+//
+// 16411 tokens of 384 experts in 13 sequences, sigmoid, BF16: 10.5 us for the
+// sums, 5.2 for the second kernel, 13.3 for the gradient (added to another), where
+// the bytes take 2.5 and 7.6. Instructions and latency bound the first (one
+// row's loads at a time, expf and divisions: 15.1 us), four dependent steps of
+// memory the second, bytes and a row's chain of two sums the third (20.7 us).
 #include "moe_rows.h"
 #include "moe_step.h"
 

@@ -11,7 +11,15 @@
 //
 // Four lanes share a block, eight values each, as in the MXFP4 kernels; a row is
 // a whole number of such quads of lanes, the last of which may have lanes
-// without values.
+// without values. All four kernels pass once over their data and are bound by it
+// (a large copy runs at 4.95 TB/s here, a fill at 6.8), BF16:
+//   mx8_quant    8192 rows of 7168: 31 us, 5.7 TB/s
+//   mx8_dequant  as 68288 rows of a routing: 212 to 222 us, 6.4 TB/s, a third of
+//                it codes that a token's eight rows read in eight XCDs
+//   swiglu_save  65536 rows of 2 x 2048: 186 us, 5.8 TB/s
+//   swiglu_grad  the same, from 8 bits: 236 us, 5.8 TB/s
+// A thread's loads all stand before its first conversion, so that they are in
+// flight together.
 #include "moe_rows.h"
 #include "moe_step.h"
 

@@ -8,7 +8,11 @@
 // Both go by tokens: a token's row of d_out is read once for its topk rows, and
 // no two tokens meet in a row (a routing's slots are distinct), so nothing is
 // added in memory. HBM bounds the large calls, the chain slot -> row -> sum the
-// small.
+// small (one token of 7168, top-8: 2.8 us). 8192 tokens of 7168, top-8, BF16: the
+// sum 188 us, 5.6 TB/s; the gradients, with the rows of 384 groups padded to 128,
+// 520 us for 1.06 GB read and 1.41 GB written, 4.8 TB/s where a copy runs at 4.95.
+// The gradients of rows pass the caches by: nothing here reads them again (561
+// us through them, padding behind the tokens).
 #include "moe_rows.h"
 #include "moe_step.h"
 
