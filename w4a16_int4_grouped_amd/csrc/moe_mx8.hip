@@ -42,10 +42,15 @@ __device__ __forceinline__ Range live_rows(const LiveRows& l, int64_t rows) {
 //   NARROW  up to 32 groups: 1 << lg threads on a row (a power of two)
 //   ROWS    up to 256 groups: the same, at least a wave on a row
 //   WIDE    longer rows: a workgroup on 256 * each groups of one row
-enum Mode : int { NARROW = 0, ROWS = 1, WIDE = 2 };
+//   FLAT    where those would leave more than a quarter of their threads idle:
+//           adjacent threads on adjacent groups, a division for each (in us for
+//           2^28 values in BF16, to 8 bits / back: rows of 264 148 / 147 against 191 /
+//           231, of 520 152 / 147 against 173 / 234, of 2056 133 / 146 against 173 /
+//           208; where rows fill their threads, of 512, 122 / 147 without it)
+enum Mode : int { NARROW = 0, ROWS = 1, WIDE = 2, FLAT = 3 };
 
 struct Shape {
-  int mode, lg, chunks;   // WIDE: chunks of a row
+  int mode, lg, chunks;   // WIDE: chunks of a row; FLAT: a row's groups
   unsigned blocks;        // workgroups, 0: too many for a grid
 };
 
@@ -53,6 +58,12 @@ Shape shape_of(int64_t rows, int n, int each) {
   Shape s{n > 256 ? WIDE : n > 32 ? ROWS : NARROW, 0, 1, 0};
   while (s.lg < 8 && (1 << s.lg) < n) ++s.lg;
   int64_t g;
+  const int span = s.mode == WIDE ? (n + 255) / 256 * 256 : 1 << s.lg;
+  if (4 * n < 3 * span && rows * n < ((int64_t)1 << 31) - 256 * each) {
+    s.mode = FLAT, s.chunks = n;
+    s.blocks = (unsigned)((rows * n + 256 * each - 1) / (256 * each));
+    return s;
+  }
   if (s.mode == WIDE) {
     s.chunks = (n + 256 * each - 1) / (256 * each);
     g = rows * s.chunks;
@@ -72,6 +83,10 @@ __device__ __forceinline__ Place place(const Shape& s, int b) {
   if constexpr (MODE == WIDE) {
     const uint32_t r = s.chunks == 1 ? blk : blk / (uint32_t)s.chunks;
     return Place{(int64_t)r, (int)(blk - r * (uint32_t)s.chunks) * (256 * EACH) + 256 * b + tid};
+  }
+  if constexpr (MODE == FLAT) {
+    const uint32_t i = (blk * EACH + b) * 256 + tid, r = i / (uint32_t)s.chunks;
+    return Place{(int64_t)r, (int)(i - r * (uint32_t)s.chunks)};
   }
   const int row = MODE == ROWS ? __builtin_amdgcn_readfirstlane(tid >> s.lg) : tid >> s.lg;
   return Place{((int64_t)blk * EACH + b) * (256 >> s.lg) + row, tid & ((1 << s.lg) - 1)};
@@ -300,7 +315,8 @@ hipError_t choose(int type, const Shape& s, F&& f) {
   auto by_mode = [&](auto ty) {
     if (s.mode == NARROW) f(ty, integral_constant<int, NARROW>{});
     else if (s.mode == ROWS) f(ty, integral_constant<int, ROWS>{});
-    else f(ty, integral_constant<int, WIDE>{});
+    else if (s.mode == WIDE) f(ty, integral_constant<int, WIDE>{});
+    else f(ty, integral_constant<int, FLAT>{});
   };
   if (type == TYPE_BF16) by_mode(integral_constant<int, TYPE_BF16>{});
   else if (type == TYPE_F16) by_mode(integral_constant<int, TYPE_F16>{});

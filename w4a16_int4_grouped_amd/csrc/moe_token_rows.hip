@@ -22,16 +22,32 @@ namespace {
 constexpr int kRowsAhead = 8;   // rows whose loads are in flight together
 
 // A thread sums 8 columns of a token. 1 << lg threads (a power of two, at most
-// 256) lie along a row, `parts` workgroups where it is longer. ROW: a wave's
-// lanes have one token, whose slots and weights are scalars. (One workgroup that
-// goes through the parts of its row measured 2.8 -> 6.3 us for a token of 7168,
-// 24 -> 25 for 1024 tokens and 96 -> 98 for 4096.)
-template <int TYPE, bool ROW>
+// 256) lie along a row, `parts` workgroups where it is longer.
+//   NARROW  less than a wave on a row
+//   ROW     a wave's lanes have one token, whose slots and weights are scalars
+//   FLAT    where several workgroups a row would leave more than a quarter of
+//           their threads idle: adjacent threads on adjacent columns, a division
+//           for each (32640 tokens of 2056, four rows each, BF16: 119 against 141 us,
+//           half as many in FP32 135 against 203; 131072 of 136, one workgroup for
+//           eight tokens, 43 against 44)
+// (One workgroup that goes through the parts of its row measured 2.8 -> 6.3 us for
+// a token of 7168, 24 -> 25 for 1024 tokens and 96 -> 98 for 4096.)
+enum Mode : int { NARROW = 0, ROW = 1, FLAT = 2 };
+
+template <int TYPE, int MODE>
 __global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type, int lg, int parts) {
-  const int blk = parts == 1 ? blockIdx.x : blockIdx.x / parts, part = blockIdx.x - blk * parts;
-  const int row = threadIdx.x >> lg;
-  const int64_t t = (int64_t)blk * (256 >> lg) + (ROW ? __builtin_amdgcn_readfirstlane(row) : row);
-  const int col = 8 * (part * 256 + (threadIdx.x & ((1 << lg) - 1)));
+  int64_t t;
+  int col;
+  if constexpr (MODE == FLAT) {
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, n = (uint32_t)p.H / 8;
+    t = i / n;
+    col = 8 * (int)(i - (uint32_t)t * n);
+  } else {
+    const int blk = parts == 1 ? blockIdx.x : blockIdx.x / parts, part = blockIdx.x - blk * parts;
+    const int row = threadIdx.x >> lg;
+    t = (int64_t)blk * (256 >> lg) + (MODE == ROW ? __builtin_amdgcn_readfirstlane(row) : row);
+    col = 8 * (part * 256 + (threadIdx.x & ((1 << lg) - 1)));
+  }
   if (t >= p.T || col >= p.H) return;
   const int32_t* slots = p.slots + t * p.topk;
   float acc[8] = {};
@@ -176,12 +192,15 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
   int lg = 0;
   while (lg < 8 && (1 << lg) < H8) ++lg;
   const int parts = (H8 + 255) / 256;
-  const int64_t g = ((int64_t)p.T + (256 >> lg) - 1) / (256 >> lg) * parts;
+  const int64_t all = (int64_t)p.T * H8;
+  const bool flat = parts > 1 && 4 * H8 < 3 * 256 * parts && all < ((int64_t)1 << 31) - 256;
+  const int64_t g = flat ? (all + 255) / 256 : ((int64_t)p.T + (256 >> lg) - 1) / (256 >> lg) * parts;
   if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   auto go = [&](auto ty) {
     constexpr int TYPE = decltype(ty)::value;
-    if (lg >= 6) combine_sum<TYPE, true><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
-    else combine_sum<TYPE, false><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
+    if (flat) combine_sum<TYPE, FLAT><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
+    else if (lg >= 6) combine_sum<TYPE, ROW><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
+    else combine_sum<TYPE, NARROW><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
   };
   if (type == TYPE_BF16) go(std::integral_constant<int, TYPE_BF16>{});
   else if (type == TYPE_F16) go(std::integral_constant<int, TYPE_F16>{});
@@ -210,7 +229,7 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
 //    2048   16384          234*   241        229    316
 // 48 experts, 16 and 64 threads:   16: all    one    64: all    one
 //      64    2048                     7.2    4.2*       7.9    7.7
-//      64   16384                      22     25*        40     55
+//      64   16384                      22*    25         40     55
 //     256    2048                      11    6.7*        14     11
 //     512    2048                      16    9.7*        17     13
 //     512   16384                      65     59*        66     80
@@ -221,7 +240,7 @@ struct Team {
 };
 Team team_of(int T, int H) {
   if (H > 2048) return T <= 128 ? Team{256, true} : T < 1024 ? Team{64, true} : Team{256, false};
-  return H > 512 ? Team{64, T < 4096} : Team{16, true};
+  return H > 512 ? Team{64, T < 4096} : Team{16, T < 8192 || H > 256};
 }
 }  // namespace
 
