@@ -16,8 +16,8 @@
 //   mx8_quant    8192 rows of 7168: 31 us, 5.7 TB/s
 //   mx8_dequant  as 68288 rows of a routing: 212 to 222 us, 6.4 TB/s, a third of
 //                it codes that a token's eight rows read in eight XCDs
-//   swiglu_save  65536 rows of 2 x 2048: 186 us, 5.8 TB/s
-//   swiglu_grad  the same, from 8 bits: 236 us, 5.8 TB/s
+//   swiglu_save  65536 rows of 2 x 2048: 180 us, 6.0 TB/s
+//   swiglu_grad  the same, from 8 bits: 232 us, 5.9 TB/s
 // A thread's loads all stand before its first conversion, so that they are in
 // flight together.
 #include "moe_rows.h"
@@ -174,7 +174,10 @@ __device__ __forceinline__ void store8_of_quad(void* x, int64_t at, const float 
   store8<TYPE>(x, at, v);
 }
 
-constexpr int kQuant = 4, kDequant = 4, kPairs = 2;   // groups per thread (pairs: of both halves)
+// Groups per thread (pairs: of both halves). In us for 1 / 2 / 4 pairs, 65536 rows
+// of 2 x 2048: kept 180 / 185 / 190, gradient 232 / 237 / 244; for 2 / 4 / 8 groups
+// 8192 rows of 7168 to 8 bits 32 / 31 / 33, back as a routing's 303 / 222 / 319.
+constexpr int kQuant = 4, kDequant = 4, kPairs = 1;
 // WIDE rows of a workgroup, where they are the many rows of a routing. In us for
 // 1 / 4 rows: 11536 rows of 7168 39 / 37, 35808 112 / 112, 68288 281 / 209, 134064
 // 639 / 518; of 4096 11552 29 / 31, 35664 80 / 79, 68512 160 / 146.
