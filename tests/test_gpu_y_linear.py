@@ -58,8 +58,8 @@ def test_linear(E, counts, N, K, dtype, act, bias, res, out_dtype):
     run(E, counts, N, K, dtype, act, bias, res, out_dtype, N + K)
 
 
-# E, rows, N, K whose form of tiles is each of the five
-FORMS = [("large", 16, 8192, 2048, 2048), ("two", 1, 1024, 4096, 512), ("four", 48, 4200, 2048, 128),
+# E, rows, N, K whose form of tiles is each of the five (tests/test_step_cpu.py asserts it)
+FORMS = [("few rows each", 64, 600, 2048, 4096), ("large", 16, 8192, 2048, 2048), ("two", 1, 1024, 4096, 512), ("four", 48, 4200, 2048, 128),
          ("split", 1, 250, 2432, 2048), ("thin", 1, 64, 512, 2048)]
 
 

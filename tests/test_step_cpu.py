@@ -3,6 +3,8 @@ call; what the binding checks of their tensors; where their outputs' memory
 comes from."""
 import contextlib
 import ctypes
+import os
+import subprocess
 import types
 
 import pytest
@@ -198,6 +200,44 @@ def test_bias_gradient_workspace(L):  # noqa: F811
     assert status == M.MOE_ERR_WORKSPACE_TOO_SMALL and str(need) in M.last_error()
     for bad in ((0, 1, 8), (4097, 1, 8), (1, -1, 8), (1, (1 << 30) + 1, 8), (1, 1, 4), (1, 1, (1 << 20) + 8)):
         assert size(*bad) == -1
+
+
+FORM_MAIN = """
+#include <cstdio>
+#include "moe_ragged_form.h"
+int main() {
+  moe::FormCall p;
+  while (std::scanf("%d %d %d %d", &p.E, &p.M, &p.I, &p.C) == 4) {
+    p.mx = p.wgrad = false, p.J = 0, p.out_size = 4;
+    std::printf("%d %d\\n", (int)moe::form_of(p), (int)moe::form_of_linear(p));
+  }
+}
+"""
+
+
+def test_forms_of_the_product_with_an_epilogue(tmp_path):
+    """Each case of the GPU test of every form takes the form it is there for; few rows an expert and a long contraction
+    take the split one where the plain product's rule would not, and nothing else changes."""
+    from tests.test_gpu_y_linear import FORMS
+    (tmp_path / "main.cpp").write_text(FORM_MAIN)
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", os.path.join(M.PKG_DIR, "csrc"), str(tmp_path / "main.cpp"),
+                    "-o", str(tmp_path / "forms")], check=True)
+
+    def forms(calls):
+        r = subprocess.run([str(tmp_path / "forms")], input="".join("%d %d %d %d\n" % c for c in calls), capture_output=True,
+                           text=True, check=True)
+        return [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
+
+    names = ["large", "two", "four", "split", "thin"]
+    for (name, *call), (plain, got) in zip(FORMS, forms([tuple(c[1:]) for c in FORMS])):
+        if name == "few rows each":
+            assert (plain, got) == (0, 3)
+        else:
+            assert names[got] == name and plain == got, name
+    few = [(48, 448, 4096, 7168), (8, 128, 14336, 4096), (384, 3584, 4096, 4096)]
+    assert all(f == (0, 3) for f in forms(few))
+    more = [(48, 1500, 4096, 7168), (48, 24576, 4096, 7168), (64, 600, 1024, 1024), (384, 4096, 7168, 256)]
+    assert all(a == b for a, b in forms(more))
 
 
 # ---- the binding ----------------------------------------------------------------------

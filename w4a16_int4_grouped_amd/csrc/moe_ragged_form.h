@@ -92,4 +92,20 @@ inline Form form_of(const FormCall& p) {
   return (Form)best;
 }
 
+// The same for a product with an epilogue. Where the weights' bytes decide,
+// form_of leaves LARGE, but experts of a few rows each and a long contraction
+// keep more loads in flight in SPLIT's many workgroups. In us, LARGE / SPLIT
+// (experts, rows in all, N, K; bias and SwiGLU, over three sets of inputs):
+//   48, 448, 4096, 7168    457 / 450      128, 1024, 1536, 2048   176 / 158
+//   48, 100, 4096, 7168    404 / 390      128, 2048, 1536, 2048   178 / 160
+//   32, 512, 4096, 4096    259 / 198      384, 3584, 4096, 4096  2232 / 2155
+//   64, 600, 2048, 4096    230 / 193      384,  448, 4096, 4096  1475 / 1518
+//   8, 128, 14336, 4096    174 / 169       24,  200, 7168, 2048   148 / 139
+// and past the border 48, 1500, 4096, 7168 463 / 492; 64, 600, 1024, 1024 29 / 32.
+inline Form form_of_linear(const FormCall& p) {
+  const Form f = form_of(p);
+  const long long live = p.E < p.M ? p.E : p.M;
+  return f == LARGE && p.M <= 16 * live && p.C >= 2048 ? SPLIT : f;
+}
+
 }  // namespace moe

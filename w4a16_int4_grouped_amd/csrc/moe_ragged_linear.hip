@@ -9,12 +9,12 @@
 // What bounds it is what bounds the plain product; the epilogue adds (us, plain
 // / bias and SwiGLU, with half the output / bias and residual, BF16):
 //   48 experts, 24576 rows, 4096 x 7168       1146 / 1151 / 1178
-//   48 experts, 448 rows, 4096 x 7168          458 / 479 / 462
+//   48 experts, 448 rows, 4096 x 7168          458 / 450 / 451 (64 x 64 tiles)
 //   384 experts, 32768 rows, 7168 x 256        352 / 390 / 475 (470 MB more to read)
 //   1 expert, 250 rows, 4864 x 7168             45 / 55 / 49
 //   8 experts, 64 rows, 1024 x 256             3.8 / 4.1 / 4.1
-// The same rule chooses the form of tiles; it took the fastest of the five or one
-// within 6 % of it at 14 such sizes.
+// form_of_linear chooses the form of tiles: the fastest of the five or one within
+// 6 % of it at 14 such sizes.
 // Measured and left out: bias and residual read before the products where the
 // contraction is split (none, and 16 -> 23 us for one row of 4096 x 7168); the
 // residual of the first 32 rows read with the first operands of 128-row tiles

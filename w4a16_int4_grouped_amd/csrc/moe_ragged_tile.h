@@ -981,7 +981,8 @@ hipError_t launch(RaggedParams p, hipStream_t s) {
   constexpr bool GLU = EPI == EPI_GLU;
   if (!QC && p.M == 0) return hipSuccess;
   const int64_t size = p.out_type == TYPE_F32 ? 4 : 2;
-  const Form f = form_of(FormCall{FMT == FMT_MX, QC, p.E, p.M, GLU ? 2 * p.I : p.I, p.J, p.C, (int)size});
+  const FormCall call{FMT == FMT_MX, QC, p.E, p.M, GLU ? 2 * p.I : p.I, p.J, p.C, (int)size};
+  const Form f = EPI != EPI_NONE ? form_of_linear(call) : form_of(call);
   const int64_t bytes = (QC ? (int64_t)p.E * p.J : p.M) * p.I * size;
   // Whole lines that the L2s (32 MB) cannot hold leave them to the operands when they pass them by: FP4, 8 experts of
   // 2048 rows 230 against 252 us. FOUR's calls are bound by such writes, and up to 256 MB the last-level cache takes
