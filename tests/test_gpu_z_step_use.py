@@ -431,3 +431,74 @@ def test_a_row_summed_more_than_once():
     out = m.combine(y.cuda(), slots.cuda(), w.cuda()).cpu()
     want = torch.stack([3 * y[0] + 3 * y[2], 10 * y[1], 0.5 * y[2] - y[0], 0 * y[0]])
     assert torch.allclose(out, want, rtol=0, atol=4 * 2.0 ** -23 * float(10 * y.abs().max()))
+
+
+# ---- the ends of the ranges ------------------------------------------------------------------
+
+
+def test_widest_rows():
+    """2^20 columns (SwiGLU 2 x 2^19)."""
+    m = M()
+    W = 1 << 20
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(3, W, generator=g).bfloat16()
+    q, s = m.mx8_quant(x.cuda())
+    val, code, byte = U.mx8(x)
+    assert torch.equal(q.cpu(), code) and torch.equal(s.cpu(), byte)
+    assert torch.equal(m.mx8_dequant(q, s).cpu(), val.bfloat16())
+    src = torch.tensor([5, 6, 0, 2, 1], dtype=torch.int32)       # of 3 x 2
+    want = torch.stack([val[2], 0 * val[0], val[0], val[1], val[0]]).bfloat16()
+    assert torch.equal(m.mx8_dequant(q, s, row_src=src.cuda(), topk=2).cpu(), want)
+    a, hq, hs = m.swiglu_save(x.cuda())
+    U.close(a, U.swiglu(x), U.swiglu_slack(x), "a")
+    d_a = torch.randn(3, W // 2, generator=g).bfloat16()
+    exact, slack = U.swiglu_grad(x, d_a)
+    U.close(m.swiglu_grad(x.cuda(), d_a.cuda())[0], exact, slack, "d_h")
+    slots = torch.tensor([[2, 0], [-1, 1]], dtype=torch.int32)
+    w = torch.tensor([[0.5, 2.0], [3.0, -1.0]])
+    out = m.combine(x.cuda(), slots.cuda(), w.cuda(), out_dtype=torch.float32).cpu().double()
+    v = x.double()
+    want = torch.stack([0.5 * v[2] + 2 * v[0], -v[1]])
+    assert ((out - want).abs() <= (0.5 * v[2].abs() + 2 * v[0].abs() + v[1].abs()) * 2.0 ** -22).all()
+    d_out = x[:2]
+    dy, dw = m.combine_grad(d_out.cuda(), slots.cuda(), y=x.cuda(), w=w.cuda())
+    d = d_out.double()
+    assert torch.equal(dy.cpu(), torch.stack([2 * d[0], -d[1], 0.5 * d[0]]).bfloat16())
+    want = torch.tensor([[float((d[0] * v[2]).sum()), float((d[0] * v[0]).sum())], [0.0, float((d[1] * v[1]).sum())]])
+    size = torch.tensor([[float((d[0] * v[2]).abs().sum()), float((d[0] * v[0]).abs().sum())], [0.0, float((d[1] * v[1]).abs().sum())]])
+    # a thread adds 2^20 / 256 products one after another, the rest are trees
+    assert ((dw.cpu().double() - want).abs() <= size * (W / 256 + 12) * 2.0 ** -24).all()
+
+
+def test_most_experts_and_sequences():
+    m = M()
+    g = torch.Generator().manual_seed(2)
+    counts = [int(c) for c in torch.randint(0, 3, (4096,), generator=g)]
+    rows = sum(counts)
+    a, w = torch.randn(rows, 8, generator=g).bfloat16(), torch.randn(4096, 16, 8, generator=g).bfloat16()
+    bias = torch.randn(4096, 16, generator=g)
+    off = offsets_of(counts).cuda()
+    for act in ("none", "swiglu"):
+        exact, slack = U.linear(a, w, counts, bias, act, None)
+        U.close(m.grouped_linear(a.cuda(), w.cuda(), off, bias=bias.cuda(), act=act), exact, slack, act)
+    dy = torch.randn(rows, 16, generator=g).bfloat16()
+    want = torch.stack([t.double().sum(0) for t in dy.split(counts)])
+    U.close(m.grouped_bias_grad(dy.cuda(), off), want, 4 * 2.0 ** -24 * 10, "bias")
+    # 2^20 sequences, nearly all empty
+    S, T, E = 1 << 20, 500, 9
+    cuts = torch.randint(0, S + 1, (T,), generator=g).sort()[0]
+    ends = torch.bincount(cuts, minlength=S + 1).cumsum(0).int()         # of sequence s: the rows drawn up to it
+    ends = torch.cat([torch.zeros(1, dtype=torch.int32), ends[:S]])
+    x = torch.randn(T, E, generator=g)
+    ids = x.topk(2, 1)[1].int()
+    loss, n = m.router_balance(x.cuda(), ids.cuda(), offsets=ends.cuda())
+    loss, n = loss.cpu(), n.cpu()
+    last = int(ends[-1])
+    assert int(n.sum()) == 2 * last and int((n.sum(1) > 0).sum()) == len(set(cuts[:last].tolist()))
+    busy = (n.sum(1) > 0).nonzero()[:, 0]
+    assert (loss[n.sum(1) == 0] == 0).all()
+    p, _ = U.scores(x, "softmax")
+    for s in busy[:40].tolist():
+        lo, hi = int(ends[s]), int(ends[s + 1])
+        want = E * (n[s].double() / (2 * (hi - lo)) * p[lo:hi].mean(0)).sum()
+        assert abs(float(loss[s]) - float(want)) <= float(want) * 64 * 2.0 ** -23
