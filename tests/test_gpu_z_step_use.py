@@ -327,6 +327,23 @@ def test_dense_rows_past_32_bits():
     assert torch.equal(m.mx8_dequant(q, s, row_src=src, out=x)[(rows - 1 - look).cuda()].cpu(), val)
 
 
+def test_more_routed_groups_than_32_bits_count():
+    """8.4 million rows of 2056 read back from four: 2^31 groups of 8, of a width that fills its threads badly."""
+    m = M()
+    K, R = 2056, 8400003
+    assert R * (K // 8) > 1 << 31
+    x = torch.randn(4, K, generator=torch.Generator().manual_seed(3)).bfloat16()
+    q, s = m.mx8_quant(x.cuda())
+    val = U.mx8(x)[0].bfloat16().cuda()
+    src = (torch.arange(R, device="cuda") * 7 % 5).int()                 # 4: no row
+    out = torch.full((R, K), 3.0, dtype=torch.bfloat16, device="cuda")
+    m.mx8_dequant(q, s, row_src=src, out=out)
+    val = torch.cat([val, torch.zeros_like(val[:1])])
+    for lo in (0, R // 4 - 20, R // 4 + 5, R // 2, R - 100):
+        assert torch.equal(out[lo: lo + 100], val[src[lo: lo + 100].long()]), lo
+    assert not (out[:, 0] == 3).any()
+
+
 def test_many_sequences_and_many_tokens():
     """More sequences than a wave looks at in one step, most of them short or empty, and chunks of many rows."""
     m = M()

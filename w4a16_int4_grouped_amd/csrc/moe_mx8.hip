@@ -373,7 +373,10 @@ hipError_t launch_mx8_quant(const void* x, int type, int64_t rows, int K, int64_
 hipError_t launch_mx8_dequant(const Mx8Rows& p, int type, hipStream_t s) {
   Shape sh = shape_of(p.out_rows, p.K / 8, kDequant);
   const bool many = sh.mode == WIDE && p.row_src && p.out_rows >= kManyRows;
-  if (many) sh = shape_of((p.out_rows + kRoutedRows - 1) / kRoutedRows, p.K / 8, kDequant);
+  if (many) {
+    const int64_t g = (p.out_rows + kRoutedRows - 1) / kRoutedRows * sh.chunks;
+    sh.blocks = g > 0x7FFFFFFF ? 0u : (unsigned)g;
+  }
   return choose(type, sh, [&](auto ty, auto mode) {
     constexpr int TYPE = decltype(ty)::value, MODE = decltype(mode)::value;
     if constexpr (MODE == WIDE)
