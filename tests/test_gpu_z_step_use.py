@@ -298,6 +298,21 @@ def test_rows_far_apart():
     assert torch.equal(m.grouped_bias_grad(far_y, off), m.grouped_bias_grad(y, off))
 
 
+def test_weights_far_apart():
+    """Gate and up halves 4.6 GB apart, rows of weights 4 MB."""
+    m = M()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    a, w, bias = r(70, 72), r(1, 2224, 72), r(1, 2224)
+    off = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    far = apart(w, (2224 * FAR, FAR, 1))
+    for act in ("swiglu", "none"):
+        assert torch.equal(m.grouped_linear(a, far, off, bias=bias, act=act), m.grouped_linear(a, w, off, bias=bias, act=act))
+    a, off = r(3000, 72), torch.tensor([0, 3000], dtype=torch.int32, device="cuda")     # larger tiles
+    assert torch.equal(m.grouped_linear(a, far, off, bias=bias, act="swiglu"),
+                       m.grouped_linear(a, w, off, bias=bias, act="swiglu"))
+
+
 def test_far_logits():
     m = M()
     x = torch.randn(600, 72, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
