@@ -1,0 +1,79 @@
+"""The step's operators at sizes whose threads one launch does not take: HIP
+refuses 2^32 of them along a dimension, sizes that the header allows have more."""
+import pytest
+import torch
+
+from tests.gpu_util import log, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def M():
+    require_gpu()
+    import w4a16_int4_grouped_amd
+    return w4a16_int4_grouped_amd
+
+
+@pytest.fixture(autouse=True)
+def memory():
+    """Each test's tens of gigabytes go back before the next asks for its own."""
+    yield
+    torch.cuda.empty_cache()
+
+
+def integers(*shape, seed):
+    return torch.randint(-3, 4, shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+
+
+@pytest.mark.parametrize("way", ["forward", "input", "bias", "swiglu"])
+def test_products_of_more_tiles_than_a_launch_takes(way):
+    """4096 experts of a row each and 2^20 columns (of weights that all share): 2^25 tiles, exact on integers."""
+    m = M()
+    E, N, K = 4096, 1 << 20, 8
+    log(f"case grouped {way} E={E} N={N} K={K}")
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda")
+    a = integers(E, K, seed=10)
+    out = torch.full((E, N // 2 if way == "swiglu" else N), 777.0, dtype=torch.bfloat16, device="cuda")
+    if way == "input":
+        w = integers(1, K, N, seed=11)
+        m.grouped_gemm_dgrad(a, w.expand(E, K, N), off, out=out)
+        w = w[0]
+    else:
+        w = integers(1, N, K, seed=11)
+        if way == "forward":
+            m.grouped_gemm(a, w.expand(E, N, K), off, out=out)
+        else:
+            bias = integers(1, N, seed=14).expand(E, N).contiguous() if way == "bias" else None
+            m.grouped_linear(a, w.expand(E, N, K), off, bias=bias, act="none" if bias is not None else way, out=out)
+        w = w[0].t()
+    for lo in range(0, E, 256):
+        z = a[lo: lo + 256].float() @ w.float()
+        if way == "bias":
+            z += bias[0].float()
+        got = out[lo: lo + 256]
+        if way == "swiglu":
+            gate, up = z[:, : N // 2], z[:, N // 2:]
+            z = gate * torch.sigmoid(gate) * up
+            # both FP32: the sigmoid within (2 |g| + 10) steps (|g| <= 72), rounded to half a step of BF16
+            assert ((got.float() - z).abs() <= z.abs() * (2.0 ** -8 + 2 * 154 * 2.0 ** -23) + 2.0 ** -126).all(), lo
+        else:
+            assert torch.equal(got.float(), z), lo
+
+
+def test_weight_gradients_of_more_tiles_than_a_launch_takes():
+    """4096 experts of 8 by 2^20."""
+    m = M()
+    E, N, K, rows = 4096, 8, 1 << 20, 5
+    log(f"case grouped wgrad E={E} N={N} K={K}")
+    dy, a = integers(rows, N, seed=12), integers(rows, K, seed=13)
+    at = torch.tensor([0, 2048, 4093, 4095])
+    counts = torch.zeros(E, dtype=torch.long)
+    counts[at] = torch.tensor([1, 2, 1, 1])
+    off = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]).int().cuda()
+    dw = torch.full((E, N, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    m.grouped_gemm_wgrad(dy, a, off, out=dw)
+    for e, lo, hi in ((0, 0, 1), (2048, 1, 3), (4093, 3, 4), (4095, 4, 5)):
+        assert torch.equal(dw[e].float(), dy[lo:hi].float().t() @ a[lo:hi].float()), e
+        dw[e] = 0
+    for lo in range(0, E, 256):
+        assert not dw[lo: lo + 256].any(), lo

@@ -45,6 +45,7 @@ struct RaggedParams {
   int64_t out_ld, out_stride;    // elements; wgrad: from expert to expert
   int out_type;
   int stream_out;         // set by the launcher: the output passes the caches by
+  uint32_t first;         //   the launch's first workgroup of the call's
   Epilogue epi;           // launch_ragged_linear (I: columns of the output, half the weights' rows with swiglu)
 };
 

@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "moe_device.h"
+#include "moe_grid.h"
 #include "moe_ragged.h"
 #include "moe_ragged_form.h"
 #include "moe_tile.h"
@@ -794,7 +795,8 @@ __attribute__((amdgpu_waves_per_eu(ONE ? 4 : 2, ONE ? 4 : 2))) void ragged_gemm(
   constexpr int BO = B4::BO;
   constexpr auto most = [](int a, int b) { return a > b ? a : b; };
   __shared__ __align__(1024) char lds[most(most(B4::kLds, B3::kLds), most(B2::kLds, B1::kLds))];
-  const Found f = QC ? even_tile(p, blockIdx.x, BJ, BO, 1) : find_tile(p, blockIdx.x, BJ, (p.I + BO - 1) / BO, 1);
+  const int b = (int)(p.first + blockIdx.x);
+  const Found f = QC ? even_tile(p, b, BJ, BO, 1) : find_tile(p, b, BJ, (p.I + BO - 1) / BO, 1);
   const Tile t = f.t;
   const Group g = f.g;
   if (t.e < 0) return;
@@ -957,8 +959,8 @@ __global__ __launch_bounds__((64 * kSplitWaves<FMT, BI>)) void ragged_split(Ragg
   __shared__ __align__(1024) char lds[Wide::kLds > Narrow::kLds ? Wide::kLds : Narrow::kLds];
   // two tiles that read the halves of the same lines on one XCD (1 expert, 64 rows, 7168 by 1024: 14.7 against 25.7 us)
   constexpr int kLeast = PC && BI == 32 ? 2 : 1;
-  const Found f = QC ? even_tile(p, blockIdx.x, 64, BO, kLeast)
-                     : find_tile(p, blockIdx.x, 64, (p.I + BO - 1) / BO, kLeast);
+  const int b = (int)(p.first + blockIdx.x);
+  const Found f = QC ? even_tile(p, b, 64, BO, kLeast) : find_tile(p, b, 64, (p.I + BO - 1) / BO, kLeast);
   const Tile t = f.t;
   const Group g = f.g;
   if (t.e < 0) return;
@@ -993,13 +995,16 @@ hipError_t launch(RaggedParams p, hipStream_t s) {
   const int64_t grid = tile_bound<QC>(p, (f == LARGE ? 256 : f == SPLIT ? 64 : f == THIN ? 32 : 128) / (GLU ? 2 : 1),
                                       f == LARGE ? 256 : f >= SPLIT ? 64 : 128);
   if (grid > 0x7FFFFFFF - kDealSlack) return hipErrorInvalidConfiguration;
-  const unsigned n = (unsigned)grid + kDealSlack;
-  if (f == LARGE) ragged_gemm<FMT, PC, QC, 256, 256, 4, 2, false, EPI><<<n, 512, 0, s>>>(p);
-  else if (f == TWO) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, false, EPI><<<n, 256, 0, s>>>(p);
-  else if (f == FOUR) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, true, EPI><<<n, 256, 0, s>>>(p);
-  else if (f == SPLIT) ragged_split<FMT, PC, QC, 64, EPI><<<n, 64 * kSplitWaves<FMT, 64>, 0, s>>>(p);
-  else ragged_split<FMT, PC, QC, 32, EPI><<<n, 64 * kSplitWaves<FMT, 32>, 0, s>>>(p);
-  return hipGetLastError();
+  const int threads = f == LARGE ? 512 : f == SPLIT ? 64 * kSplitWaves<FMT, 64> : f == THIN ? 64 * kSplitWaves<FMT, 32> : 256;
+  return in_slices(grid + kDealSlack, threads, [&](uint32_t first, uint32_t n) {
+    p.first = first;
+    if (f == LARGE) ragged_gemm<FMT, PC, QC, 256, 256, 4, 2, false, EPI><<<n, threads, 0, s>>>(p);
+    else if (f == TWO) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, false, EPI><<<n, threads, 0, s>>>(p);
+    else if (f == FOUR) ragged_gemm<FMT, PC, QC, 128, 128, 2, 2, true, EPI><<<n, threads, 0, s>>>(p);
+    else if (f == SPLIT) ragged_split<FMT, PC, QC, 64, EPI><<<n, threads, 0, s>>>(p);
+    else ragged_split<FMT, PC, QC, 32, EPI><<<n, threads, 0, s>>>(p);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
