@@ -3,6 +3,7 @@ refuses 2^32 of them along a dimension, sizes that the header allows have more."
 import pytest
 import torch
 
+from tests import step_util as U
 from tests.gpu_util import log, require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -19,6 +20,43 @@ def memory():
     """Each test's tens of gigabytes go back before the next asks for its own."""
     yield
     torch.cuda.empty_cache()
+
+
+def test_padding_of_more_rows_than_a_launch_takes():
+    """2^28 rows, nearly all of them padding."""
+    m = M()
+    R, H, T = (1 << 28) + 5, 8, 3
+    log(f"case combine_grad R={R} H={H}")
+    d = torch.randn(T, H, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    slots = torch.tensor([[R - 1], [0], [1 << 27]], dtype=torch.int32, device="cuda")
+    src = torch.full((R,), T, dtype=torch.int32, device="cuda")
+    src[slots[:, 0].long()] = torch.arange(T, dtype=torch.int32, device="cuda")
+    dy, _ = m.combine_grad(d, slots, row_src=src, out=(torch.full((R, H), 3.0, dtype=torch.bfloat16, device="cuda"), None))
+    assert torch.equal(dy[slots[:, 0].long()], d)
+    dy[slots[:, 0].long()] = 0
+    for lo in range(0, R, 1 << 26):
+        assert not dy[lo: lo + (1 << 26)].any(), lo
+
+
+def test_gradients_of_more_tokens_than_a_launch_takes():
+    """2^24 tokens of 16 rows, 16 threads a row; few of the rows are there."""
+    m = M()
+    T, topk, H, R = 1 << 24, 16, 264, 70
+    log(f"case combine_grad T={T} topk={topk} H={H}")
+    g = torch.Generator().manual_seed(4)
+    row = torch.randn(3, H, generator=g).bfloat16().cuda()
+    d = row[torch.arange(T, device="cuda") % 3]
+    y = torch.randn(R, H, generator=g).bfloat16()
+    slots = torch.full((T, topk), -1, dtype=torch.int32, device="cuda")
+    t = torch.linspace(0, T - 1, R, dtype=torch.float64).long()
+    j = torch.arange(R) % topk
+    slots[t.cuda(), j.cuda()] = torch.arange(R, dtype=torch.int32, device="cuda")
+    dy, dw = m.combine_grad(d, slots, y=y.cuda())
+    want = row.cpu()[t % 3]
+    assert torch.equal(dy.cpu(), want)
+    prod = want.double() * y.double()
+    U.close(dw[t.cuda(), j.cuda()], prod.sum(1), prod.abs().sum(1) * (H + 1) * 2.0 ** -24, "d_w")
+    assert int((dw != 0).sum()) == R
 
 
 def integers(*shape, seed):

@@ -13,6 +13,7 @@
 // 520 us for 1.06 GB read and 1.41 GB written, 4.8 TB/s where a copy runs at 4.95.
 // The gradients of rows pass the caches by: nothing here reads them again (561
 // us through them, padding behind the tokens).
+#include "moe_grid.h"
 #include "moe_rows.h"
 #include "moe_step.h"
 
@@ -97,17 +98,20 @@ __device__ __forceinline__ float team_sum(float v) {
 }
 
 // TEAM threads (16, 64 or 256) take `each` of a token's rows, 16 threads only of
-// up to 512 columns. The first workgroups look through kPadRows rows each for
-// such as no token names and write 0 there.
+// up to 512 columns. The call's first workgroups (this launch's begin with
+// `first`) look through kPadRows rows each for such as no token names and write
+// 0 there.
 template <int TYPE, int TEAM>
-__global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, int each, int pad_blocks) {
+__global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, int each, int pad_blocks,
+                                                    uint32_t first) {
   __shared__ float sums[4][64];   // TEAM 256: of a wave, per row
+  const int blk = (int)(first + blockIdx.x);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if ((int)blockIdx.x < pad_blocks) {
+  if (blk < pad_blocks) {
     const int lo = p.offsets ? max(p.offsets[0], 0) : 0, hi = p.offsets ? min(p.offsets[p.E], p.R) : p.R;
     const float zero[8] = {};
     int src[kPadRows / 4];
-    const int64_t r0 = (int64_t)blockIdx.x * kPadRows + wave * (kPadRows / 4);
+    const int64_t r0 = (int64_t)blk * kPadRows + wave * (kPadRows / 4);
 #pragma unroll
     for (int i = 0; i < kPadRows / 4; ++i) src[i] = r0 + i >= lo && r0 + i < hi ? p.row_src[r0 + i] : 0;
     for (int i = 0; i < kPadRows / 4; ++i) {
@@ -116,7 +120,7 @@ __global__ __launch_bounds__(256) void combine_grad(CombineParams p, int parts, 
     }
     return;
   }
-  const int64_t block = (int)blockIdx.x - pad_blocks;
+  const int64_t block = blk - pad_blocks;
   const int64_t team = TEAM == 16 ? (block * 4 + wave) * 4 + lane / 16 : TEAM == 64 ? block * 4 + wave : block;
   const int64_t t = parts == 1 ? team : (uint32_t)team / (uint32_t)parts;
   const int id = TEAM == 16 ? lane % 16 : TEAM == 64 ? lane : threadIdx.x;
@@ -251,17 +255,18 @@ hipError_t launch_combine_grad(const CombineParams& p, int type, hipStream_t s) 
   const int pads = p.row_src ? (p.R + kPadRows - 1) / kPadRows : 0;
   const int64_t g = blocks + pads;
   if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  if (g == 0) return hipSuccess;
   auto go = [&](auto ty) {
     constexpr int TYPE = decltype(ty)::value;
-    if (m.threads == 256) combine_grad<TYPE, 256><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
-    else if (m.threads == 64) combine_grad<TYPE, 64><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
-    else combine_grad<TYPE, 16><<<(unsigned)g, 256, 0, s>>>(p, parts, each, pads);
+    return in_slices(g, 256, [&](uint32_t first, uint32_t n) {
+      if (m.threads == 256) combine_grad<TYPE, 256><<<n, 256, 0, s>>>(p, parts, each, pads, first);
+      else if (m.threads == 64) combine_grad<TYPE, 64><<<n, 256, 0, s>>>(p, parts, each, pads, first);
+      else combine_grad<TYPE, 16><<<n, 256, 0, s>>>(p, parts, each, pads, first);
+      return hipGetLastError();
+    });
   };
-  if (type == TYPE_BF16) go(std::integral_constant<int, TYPE_BF16>{});
-  else if (type == TYPE_F16) go(std::integral_constant<int, TYPE_F16>{});
-  else go(std::integral_constant<int, TYPE_F32>{});
-  return hipGetLastError();
+  if (type == TYPE_BF16) return go(std::integral_constant<int, TYPE_BF16>{});
+  if (type == TYPE_F16) return go(std::integral_constant<int, TYPE_F16>{});
+  return go(std::integral_constant<int, TYPE_F32>{});
 }
 
 }  // namespace moe
