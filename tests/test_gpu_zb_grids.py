@@ -22,6 +22,20 @@ def memory():
     torch.cuda.empty_cache()
 
 
+def test_combine_of_more_tokens_than_a_launch_takes():
+    """2^24 tokens of 1032 columns, a workgroup each."""
+    m = M()
+    T, H, R = 1 << 24, 1032, 5
+    log(f"case combine T={T} H={H}")
+    y = torch.randn(R, H, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    slots = (torch.arange(T, device="cuda") * 7 % (R + 1)).int()          # R: no row
+    out = m.combine(y, slots[:, None])
+    rows = torch.cat([y, torch.zeros_like(y[:1])])
+    for lo in range(0, T, 1 << 21):
+        hi = lo + (1 << 21)
+        assert torch.equal(out[lo:hi], rows[slots[lo:hi].long()]), lo
+
+
 def test_padding_of_more_rows_than_a_launch_takes():
     """2^28 rows, nearly all of them padding."""
     m = M()

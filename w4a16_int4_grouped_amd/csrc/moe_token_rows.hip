@@ -36,15 +36,17 @@ constexpr int kRowsAhead = 8;   // rows whose loads are in flight together
 enum Mode : int { NARROW = 0, ROW = 1, FLAT = 2 };
 
 template <int TYPE, int MODE>
-__global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type, int lg, int parts) {
+__global__ __launch_bounds__(256) void combine_sum(CombineParams p, int out_type, int lg, int parts,
+                                                   uint32_t first) {
+  const uint32_t wg = first + blockIdx.x;   // of the call's
   int64_t t;
   int col;
   if constexpr (MODE == FLAT) {
-    const uint32_t i = blockIdx.x * 256 + threadIdx.x, n = (uint32_t)p.H / 8;
+    const uint32_t i = wg * 256 + threadIdx.x, n = (uint32_t)p.H / 8;
     t = i / n;
     col = 8 * (int)(i - (uint32_t)t * n);
   } else {
-    const int blk = parts == 1 ? blockIdx.x : blockIdx.x / parts, part = blockIdx.x - blk * parts;
+    const int blk = parts == 1 ? wg : wg / parts, part = wg - blk * parts;
     const int row = threadIdx.x >> lg;
     t = (int64_t)blk * (256 >> lg) + (MODE == ROW ? __builtin_amdgcn_readfirstlane(row) : row);
     col = 8 * (part * 256 + (threadIdx.x & ((1 << lg) - 1)));
@@ -202,14 +204,16 @@ hipError_t launch_combine_out(const CombineParams& p, int type, int out_type, hi
   if (g > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   auto go = [&](auto ty) {
     constexpr int TYPE = decltype(ty)::value;
-    if (flat) combine_sum<TYPE, FLAT><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
-    else if (lg >= 6) combine_sum<TYPE, ROW><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
-    else combine_sum<TYPE, NARROW><<<(unsigned)g, 256, 0, s>>>(p, out_type, lg, parts);
+    return in_slices(g, 256, [&](uint32_t first, uint32_t n) {
+      if (flat) combine_sum<TYPE, FLAT><<<n, 256, 0, s>>>(p, out_type, lg, parts, first);
+      else if (lg >= 6) combine_sum<TYPE, ROW><<<n, 256, 0, s>>>(p, out_type, lg, parts, first);
+      else combine_sum<TYPE, NARROW><<<n, 256, 0, s>>>(p, out_type, lg, parts, first);
+      return hipGetLastError();
+    });
   };
-  if (type == TYPE_BF16) go(std::integral_constant<int, TYPE_BF16>{});
-  else if (type == TYPE_F16) go(std::integral_constant<int, TYPE_F16>{});
-  else go(std::integral_constant<int, TYPE_F32>{});
-  return hipGetLastError();
+  if (type == TYPE_BF16) return go(std::integral_constant<int, TYPE_BF16>{});
+  if (type == TYPE_F16) return go(std::integral_constant<int, TYPE_F16>{});
+  return go(std::integral_constant<int, TYPE_F32>{});
 }
 
 // Threads of a team, and whether it takes a token's rows one by one. Measured in
