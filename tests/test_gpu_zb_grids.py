@@ -73,6 +73,72 @@ def test_gradients_of_more_tokens_than_a_launch_takes():
     assert int((dw != 0).sum()) == R
 
 
+def test_rows_to_8_bits_of_more_than_a_launch_takes():
+    """2^24 rows of 2056, a workgroup each."""
+    m = M()
+    rows, K, n = 1 << 24, 2056, 1 << 12
+    log(f"case mx8_quant rows={rows} K={K}")
+    some = torch.randn(n, K, generator=torch.Generator().manual_seed(5)).bfloat16()
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+    x.view(-1, n, K)[:] = some.cuda()
+    q, s = m.mx8_quant(x)
+    _, code, byte = U.mx8(some)
+    code, byte = code.cuda(), byte.cuda()
+    for lo in range(0, rows, n):
+        assert torch.equal(q[lo: lo + n], code) and torch.equal(s[lo: lo + n, : byte.shape[1]], byte), lo
+
+
+def test_rows_from_8_bits_of_more_than_a_launch_takes():
+    """2^24 rows of 2056 of which the last are live: the others are not touched."""
+    m = M()
+    rows, K, n = 1 << 24, 2056, 1000
+    log(f"case mx8_dequant rows={rows} K={K}")
+    some = torch.randn(n, K, generator=torch.Generator().manual_seed(6)).bfloat16()
+    q = torch.empty(rows, K, dtype=torch.int8, device="cuda")
+    s = torch.empty(rows, m.mx8_scale_cols(K), dtype=torch.uint8, device="cuda")
+    m.mx8_quant(some.cuda(), out=(q[-n:], s[-n:]))
+    out = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+    out[-n - 5:] = 3
+    live = torch.tensor([rows - n, rows], dtype=torch.int32, device="cuda")
+    m.mx8_dequant(q, s, offsets=live, out=out)
+    assert torch.equal(out[-n:].cpu(), U.mx8(some)[0].bfloat16()) and (out[-n - 5: -n] == 3).all()
+
+
+def test_swiglu_of_more_rows_than_a_launch_takes():
+    """2^30 rows of 8 of which the last are live, four threads each."""
+    m = M()
+    rows, I, n = 1 << 30, 8, 1000
+    log(f"case swiglu_save rows={rows} I={I}")
+    some = torch.randn(n, 2 * I, generator=torch.Generator().manual_seed(7)).bfloat16()
+    h = torch.empty(rows, 2 * I, dtype=torch.bfloat16, device="cuda")
+    h[-n:] = some.cuda()
+    live = torch.tensor([rows - n, rows], dtype=torch.int32, device="cuda")
+    a, q, s = m.swiglu_save(h, offsets=live)
+    U.close(a[-n:], U.swiglu(some), U.swiglu_slack(some), "a")
+    _, code, byte = U.mx8(some.view(2 * n, I))
+    assert torch.equal(q[-n:].cpu(), code.view(n, 2, I)) and torch.equal(s[-n:, :, :1].cpu(), byte.view(n, 2, 1))
+
+
+def test_swiglu_gradient_of_more_rows_than_a_launch_takes():
+    """17 million rows of 1032 of which the last are live, a workgroup each."""
+    m = M()
+    rows, I, n = 17_000_003, 1032, 1000
+    log(f"case swiglu_grad rows={rows} I={I}")
+    g = torch.Generator().manual_seed(8)
+    some = torch.randn(n, 2 * I, generator=g).bfloat16()
+    d = torch.randn(n, I, generator=g).bfloat16()
+    q = torch.empty(rows, 2, I, dtype=torch.int8, device="cuda")
+    s = torch.empty(rows, 2, m.mx8_scale_cols(I), dtype=torch.uint8, device="cuda")
+    code, byte = m.mx8_quant(some.cuda().view(2 * n, I))
+    q[-n:], s[-n:] = code.view(n, 2, I), byte.view(n, 2, -1)
+    d_a = torch.empty(rows, I, dtype=torch.bfloat16, device="cuda")
+    d_a[-n:] = d.cuda()
+    live = torch.tensor([rows - n, rows], dtype=torch.int32, device="cuda")
+    d_h, _ = m.swiglu_grad(q, d_a, scales=s, offsets=live, need_a=False)
+    exact, slack = U.swiglu_grad(U.mx8(some.view(2 * n, I))[0].view(n, 2 * I), d)
+    U.close(d_h[-n:], exact, slack, "d_h")
+
+
 def integers(*shape, seed):
     return torch.randint(-3, 4, shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
 

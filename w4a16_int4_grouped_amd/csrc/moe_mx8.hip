@@ -20,6 +20,7 @@
 //   swiglu_grad  the same, from 8 bits: 232 us, 5.9 TB/s
 // A thread's loads all stand before its first conversion, so that they are in
 // flight together.
+#include "moe_grid.h"
 #include "moe_rows.h"
 #include "moe_step.h"
 
@@ -51,11 +52,12 @@ enum Mode : int { NARROW = 0, ROWS = 1, WIDE = 2, FLAT = 3 };
 
 struct Shape {
   int mode, lg, chunks;   // WIDE: chunks of a row; FLAT: a row's groups
-  unsigned blocks;        // workgroups, 0: too many for a grid
+  unsigned blocks;        // workgroups, 0: more than 2^31 - 1
+  uint32_t first;         // of a launch, among the call's
 };
 
 Shape shape_of(int64_t rows, int n, int each) {
-  Shape s{n > 256 ? WIDE : n > 32 ? ROWS : NARROW, 0, 1, 0};
+  Shape s{n > 256 ? WIDE : n > 32 ? ROWS : NARROW, 0, 1, 0, 0};
   while (s.lg < 8 && (1 << s.lg) < n) ++s.lg;
   int64_t g;
   const int span = s.mode == WIDE ? (n + 255) / 256 * 256 : 1 << s.lg;
@@ -78,7 +80,7 @@ Shape shape_of(int64_t rows, int n, int each) {
 // Row and group of a thread's b-th place.
 template <int MODE, int EACH>
 __device__ __forceinline__ Place place(const Shape& s, int b) {
-  const uint32_t blk = blockIdx.x;
+  const uint32_t blk = s.first + blockIdx.x;
   const int tid = threadIdx.x;
   if constexpr (MODE == WIDE) {
     const uint32_t r = s.chunks == 1 ? blk : blk / (uint32_t)s.chunks;
@@ -340,21 +342,25 @@ __global__ __launch_bounds__(256) void swiglu_grad(SwigluParams s, Shape sh) {
   }
 }
 
-// f(TYPE, MODE) for a call's type and shape.
+// f(TYPE, MODE, shape) for a call's type and shape, once for each launch that it
+// takes, whose workgroups the shape passed on has.
 template <class F>
-hipError_t choose(int type, const Shape& s, F&& f) {
+hipError_t choose(int type, Shape s, F&& f) {
   using std::integral_constant;
   if (!s.blocks) return hipErrorInvalidConfiguration;
   auto by_mode = [&](auto ty) {
-    if (s.mode == NARROW) f(ty, integral_constant<int, NARROW>{});
-    else if (s.mode == ROWS) f(ty, integral_constant<int, ROWS>{});
-    else if (s.mode == WIDE) f(ty, integral_constant<int, WIDE>{});
-    else f(ty, integral_constant<int, FLAT>{});
+    if (s.mode == NARROW) f(ty, integral_constant<int, NARROW>{}, s);
+    else if (s.mode == ROWS) f(ty, integral_constant<int, ROWS>{}, s);
+    else if (s.mode == WIDE) f(ty, integral_constant<int, WIDE>{}, s);
+    else f(ty, integral_constant<int, FLAT>{}, s);
   };
-  if (type == TYPE_BF16) by_mode(integral_constant<int, TYPE_BF16>{});
-  else if (type == TYPE_F16) by_mode(integral_constant<int, TYPE_F16>{});
-  else by_mode(integral_constant<int, TYPE_F32>{});
-  return hipGetLastError();
+  return in_slices(s.blocks, 256, [&](uint32_t first, uint32_t n) {
+    s.first = first, s.blocks = n;
+    if (type == TYPE_BF16) by_mode(integral_constant<int, TYPE_BF16>{});
+    else if (type == TYPE_F16) by_mode(integral_constant<int, TYPE_F16>{});
+    else by_mode(integral_constant<int, TYPE_F32>{});
+    return hipGetLastError();
+  });
 }
 // Lanes of a row whose blocks of 32 are found by four lanes each.
 int quads(int n8) { return (n8 + 3) & ~3; }
@@ -363,21 +369,21 @@ int quads(int n8) { return (n8 + 3) & ~3; }
 
 hipError_t launch_mx8_quant(const void* x, int type, int64_t rows, int K, int64_t ld, int8_t* q, uint8_t* scales,
                             int s_ld, hipStream_t s) {
-  const Shape sh = shape_of(rows, quads(K / 8), kQuant);
-  return choose(type, sh, [&](auto ty, auto mode) {
+  const Shape shape = shape_of(rows, quads(K / 8), kQuant);
+  return choose(type, shape, [&](auto ty, auto mode, const Shape& sh) {
     mx8_quant<decltype(ty)::value, decltype(mode)::value><<<sh.blocks, 256, 0, s>>>(x, rows, K / 8, ld, q, scales, s_ld,
                                                                                     sh);
   });
 }
 
 hipError_t launch_mx8_dequant(const Mx8Rows& p, int type, hipStream_t s) {
-  Shape sh = shape_of(p.out_rows, p.K / 8, kDequant);
-  const bool many = sh.mode == WIDE && p.row_src && p.out_rows >= kManyRows;
+  Shape shape = shape_of(p.out_rows, p.K / 8, kDequant);
+  const bool many = shape.mode == WIDE && p.row_src && p.out_rows >= kManyRows;
   if (many) {
-    const int64_t g = (p.out_rows + kRoutedRows - 1) / kRoutedRows * sh.chunks;
-    sh.blocks = g > 0x7FFFFFFF ? 0u : (unsigned)g;
+    const int64_t g = (p.out_rows + kRoutedRows - 1) / kRoutedRows * shape.chunks;
+    shape.blocks = g > 0x7FFFFFFF ? 0u : (unsigned)g;
   }
-  return choose(type, sh, [&](auto ty, auto mode) {
+  return choose(type, shape, [&](auto ty, auto mode, const Shape& sh) {
     constexpr int TYPE = decltype(ty)::value, MODE = decltype(mode)::value;
     if constexpr (MODE == WIDE)
       if (many) return mx8_dequant<TYPE, MODE, kRoutedRows><<<sh.blocks, 256, 0, s>>>(p, sh);
@@ -386,15 +392,15 @@ hipError_t launch_mx8_dequant(const Mx8Rows& p, int type, hipStream_t s) {
 }
 
 hipError_t launch_swiglu_save(const SwigluParams& p, int type, hipStream_t s) {
-  const Shape sh = shape_of(p.rows, quads(p.I / 8), kPairs);
-  return choose(type, sh, [&](auto ty, auto mode) {
+  const Shape shape = shape_of(p.rows, quads(p.I / 8), kPairs);
+  return choose(type, shape, [&](auto ty, auto mode, const Shape& sh) {
     swiglu_save<decltype(ty)::value, decltype(mode)::value><<<sh.blocks, 256, 0, s>>>(p, sh);
   });
 }
 
 hipError_t launch_swiglu_grad(const SwigluParams& p, int type, hipStream_t s) {
-  const Shape sh = shape_of(p.rows, p.I / 8, kPairs);
-  return choose(type, sh, [&](auto ty, auto mode) {
+  const Shape shape = shape_of(p.rows, p.I / 8, kPairs);
+  return choose(type, shape, [&](auto ty, auto mode, const Shape& sh) {
     constexpr int TYPE = decltype(ty)::value, MODE = decltype(mode)::value;
     if (p.h) swiglu_grad<TYPE, MODE, false><<<sh.blocks, 256, 0, s>>>(p, sh);
     else swiglu_grad<TYPE, MODE, true><<<sh.blocks, 256, 0, s>>>(p, sh);
