@@ -116,7 +116,7 @@ def test_swiglu_of_more_rows_than_a_launch_takes():
     a, q, s = m.swiglu_save(h, offsets=live)
     U.close(a[-n:], U.swiglu(some), U.swiglu_slack(some), "a")
     _, code, byte = U.mx8(some.view(2 * n, I))
-    assert torch.equal(q[-n:].cpu(), code.view(n, 2, I)) and torch.equal(s[-n:, :, :1].cpu(), byte.view(n, 2, 1))
+    assert torch.equal(q[-n:].cpu(), code.reshape(n, 2, I)) and torch.equal(s[-n:, :, :1].cpu(), byte.reshape(n, 2, 1))
 
 
 def test_swiglu_gradient_of_more_rows_than_a_launch_takes():
@@ -135,7 +135,7 @@ def test_swiglu_gradient_of_more_rows_than_a_launch_takes():
     d_a[-n:] = d.cuda()
     live = torch.tensor([rows - n, rows], dtype=torch.int32, device="cuda")
     d_h, _ = m.swiglu_grad(q, d_a, scales=s, offsets=live, need_a=False)
-    exact, slack = U.swiglu_grad(U.mx8(some.view(2 * n, I))[0].view(n, 2 * I), d)
+    exact, slack = U.swiglu_grad(U.mx8(some.view(2 * n, I))[0].reshape(n, 2 * I), d)
     U.close(d_h[-n:], exact, slack, "d_h")
 
 
