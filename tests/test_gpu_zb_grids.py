@@ -22,6 +22,26 @@ def memory():
     torch.cuda.empty_cache()
 
 
+def test_more_sequences_by_experts_than_a_launch_takes():
+    """2^20 sequences of 200 experts: 2^22 workgroups of 1024 threads join the sums."""
+    m = M()
+    T, E, topk, S = 3000, 200, 4, 1 << 20
+    log(f"case balance T={T} E={E} S={S}")
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(T, E, generator=g)
+    ids = x.topk(topk, 1)[1].int()
+    ends = torch.randint(0, T + 1, (S + 1,), generator=g).sort()[0].int()
+    ends[0], ends[-1] = 0, T
+    loss, counts = m.router_balance(x.cuda(), ids.cuda(), offsets=ends.cuda())
+    full = (ends[1:] > ends[:-1]).nonzero()[:, 0]
+    lens = torch.cat([ends[:1], ends[1:][full]])
+    want, n = U.balance(x, ids, "softmax", lens)
+    assert torch.equal(counts[full.cuda()].cpu(), n) and int(counts.sum()) == T * topk
+    rel = float(U.score_error(x).max()) + 160 * 2.0 ** -24
+    U.close(loss[full.cuda()], want, want.abs() * rel, "loss")
+    assert int((loss != 0).sum()) == len(full)
+
+
 def test_combine_of_more_tokens_than_a_launch_takes():
     """2^24 tokens of 1032 columns, a workgroup each."""
     m = M()

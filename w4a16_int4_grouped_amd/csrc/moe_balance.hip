@@ -283,14 +283,15 @@ __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceW
   }
 }
 
-// Sequence blockIdx.x / groups, 64 experts. The last workgroup of a sequence
-// adds up the shares of its loss, in their order.
+// Sequence blockIdx.x, 64 experts. The last workgroup of a sequence adds up the
+// shares of its loss, in their order. (2^20 sequences of 4 groups in one dimension
+// would be 2^32 threads, which a launch does not take.)
 constexpr int kFinishWaves = 16;
 __global__ __launch_bounds__(64 * kFinishWaves) void balance_finish(BalanceParams p, BalanceWs ws) {
   __shared__ double part[kFinishWaves][64];
   __shared__ int num[kFinishWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int s = blockIdx.x / ws.groups, g = blockIdx.x - s * ws.groups;
+  const int s = blockIdx.x, g = blockIdx.y;
   const int e = 64 * g + lane;
   char* const base = static_cast<char*>(p.ws);
   const Rows q = sequence(p, s);
@@ -459,7 +460,7 @@ hipError_t launch_balance(const BalanceParams& p, int type, hipStream_t s) {
     });
   });
   if (e != hipSuccess || solo) return e;
-  balance_finish<<<(unsigned)(p.S * ws.groups), 64 * kFinishWaves, 0, s>>>(p, ws);
+  balance_finish<<<dim3((unsigned)p.S, (unsigned)ws.groups), 64 * kFinishWaves, 0, s>>>(p, ws);
   return hipGetLastError();
 }
 
