@@ -159,6 +159,22 @@ def test_swiglu_gradient_of_more_rows_than_a_launch_takes():
     U.close(d_h[-n:], exact, slack, "d_h")
 
 
+def test_biases_of_more_experts_by_columns_than_a_launch_takes():
+    """4096 experts of 2^17 columns: 2^23 workgroups of 512 threads."""
+    m = M()
+    E, N, rows = 4096, 1 << 17, 9
+    log(f"case grouped_bias_grad E={E} N={N}")
+    dy = torch.randn(rows, N, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    at = torch.tensor([0, 1, 700, 2047, 2048, 3000, 4000, 4094, 4095])    # one row each
+    counts = torch.zeros(E, dtype=torch.long)
+    counts[at] = 1
+    off = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]).int().cuda()
+    db = m.grouped_bias_grad(dy, off, out=torch.full((E, N), 3.0, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(db[at.cuda()], dy)
+    db[at.cuda()] = 0
+    assert not db.any()
+
+
 def integers(*shape, seed):
     return torch.randint(-3, 4, shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
 

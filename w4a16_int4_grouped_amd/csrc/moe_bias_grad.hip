@@ -8,6 +8,7 @@
 // 64 columns of a chunk for each group in it, and a second kernel adds the
 // chunks' sums up. Part c + e of the workspace belongs to chunk c and group e; no
 // two such pairs have the same sum, because both only grow along the rows.
+#include "moe_grid.h"
 #include "moe_rows.h"
 #include "moe_step.h"
 
@@ -74,20 +75,20 @@ __device__ __forceinline__ void store_any(void* x, int64_t at, int type, float v
 }
 
 template <int TYPE>
-__global__ __launch_bounds__(64 * kWaves) void bias_grad(BiasGradParams p, int out_type, int blocks) {
+__global__ __launch_bounds__(64 * kWaves) void bias_grad(BiasGradParams p, int out_type, int blocks, uint32_t first) {
   __shared__ float part[kWaves][64];
-  const int e = blockIdx.x / blocks, c0 = (blockIdx.x - e * blocks) * 64;
+  const int wg = (int)(first + blockIdx.x), e = wg / blocks, c0 = (wg - e * blocks) * 64;
   const Rows g = group(p, e);
   const float v = column_sum<TYPE>(p, c0, g.lo, g.hi, part);
   if (threadIdx.x < 64 && c0 + (int)threadIdx.x < p.N)
     store_any(p.db, (int64_t)e * p.db_ld + c0 + threadIdx.x, out_type, v);
 }
 
-// Chunk blockIdx.x / blocks; the groups in it, the first found by halves.
+// A chunk of rows by 64 columns; the groups in it, the first found by halves.
 template <int TYPE>
-__global__ __launch_bounds__(64 * kWaves) void bias_grad_parts(BiasGradParams p, int blocks) {
+__global__ __launch_bounds__(64 * kWaves) void bias_grad_parts(BiasGradParams p, int blocks, uint32_t first) {
   __shared__ float part[kWaves][64];
-  const int c = blockIdx.x / blocks, c0 = (blockIdx.x - c * blocks) * 64;
+  const int wg = (int)(first + blockIdx.x), c = wg / blocks, c0 = (wg - c * blocks) * 64;
   const int r0 = c * kChunk, r1 = min((int64_t)r0 + kChunk, (int64_t)p.M);
   int a = 0, b = p.E;
   while (a < b) {
@@ -107,10 +108,11 @@ __global__ __launch_bounds__(64 * kWaves) void bias_grad_parts(BiasGradParams p,
   }
 }
 
-__global__ __launch_bounds__(64 * kWaves) void bias_grad_finish(BiasGradParams p, int out_type, int blocks) {
+__global__ __launch_bounds__(64 * kWaves) void bias_grad_finish(BiasGradParams p, int out_type, int blocks,
+                                                               uint32_t first) {
   __shared__ float part[kWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.x / blocks, col = (blockIdx.x - e * blocks) * 64 + lane;
+  const int wg = (int)(first + blockIdx.x), e = wg / blocks, col = (wg - e * blocks) * 64 + lane;
   const Rows g = group(p, e);
   float v = 0.f;
   if (g.lo < g.hi && col < p.N) {
@@ -151,17 +153,24 @@ hipError_t launch_bias_grad(const BiasGradParams& p, int type, int out_type, hip
   const int blocks = (p.N + 63) / 64;
   const int64_t groups = (int64_t)p.E * blocks, parts = chunks_of(p.M) * blocks;
   if (groups > 0x7FFFFFFF || parts > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  constexpr int kThreads = 64 * kWaves;
   if (!cut(p.E, p.M, p.N)) {
-    if (type == TYPE_BF16) bias_grad<TYPE_BF16><<<(unsigned)groups, 64 * kWaves, 0, s>>>(p, out_type, blocks);
-    else bias_grad<TYPE_F16><<<(unsigned)groups, 64 * kWaves, 0, s>>>(p, out_type, blocks);
-    return hipGetLastError();
+    return in_slices(groups, kThreads, [&](uint32_t first, uint32_t n) {
+      if (type == TYPE_BF16) bias_grad<TYPE_BF16><<<n, kThreads, 0, s>>>(p, out_type, blocks, first);
+      else bias_grad<TYPE_F16><<<n, kThreads, 0, s>>>(p, out_type, blocks, first);
+      return hipGetLastError();
+    });
   }
-  if (type == TYPE_BF16) bias_grad_parts<TYPE_BF16><<<(unsigned)parts, 64 * kWaves, 0, s>>>(p, blocks);
-  else bias_grad_parts<TYPE_F16><<<(unsigned)parts, 64 * kWaves, 0, s>>>(p, blocks);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = in_slices(parts, kThreads, [&](uint32_t first, uint32_t n) {
+    if (type == TYPE_BF16) bias_grad_parts<TYPE_BF16><<<n, kThreads, 0, s>>>(p, blocks, first);
+    else bias_grad_parts<TYPE_F16><<<n, kThreads, 0, s>>>(p, blocks, first);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return e;
-  bias_grad_finish<<<(unsigned)groups, 64 * kWaves, 0, s>>>(p, out_type, blocks);
-  return hipGetLastError();
+  return in_slices(groups, kThreads, [&](uint32_t first, uint32_t n) {
+    bias_grad_finish<<<n, kThreads, 0, s>>>(p, out_type, blocks, first);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace moe
