@@ -191,8 +191,16 @@ __device__ __forceinline__ void scores(float (&l)[VPL], int sigmoid_scores, floa
 // Rows of a wave whose loads are in flight together.
 constexpr int rows_ahead(int VPL) { return VPL <= 8 ? 4 : VPL <= 16 ? 2 : 1; }
 
-// W waves sum a chunk. SOLO: the one chunk of the one sequence: counts and loss at once.
-template <int TYPE, int VPL, int V, int W, bool SOLO>
+// Rows that a wave adds up in registers one after another; its sum of more is
+// (LONG) one of such sums, in LDS. All terms have one sign: 2^24 tokens of even
+// scores, 2048 a wave for 13 experts, were off by 434 2^-24 in one chain of FP32.
+// LONG's branch in all kernels cost shorter chunks up to 4 % (512 tokens of 4096
+// experts 14.5 -> 15.1 us).
+constexpr int kFold = 128;
+
+// W waves sum a chunk. SOLO: the one chunk of the one sequence: counts and loss at
+// once. LONG: of more than kFold rows a wave.
+template <int TYPE, int VPL, int V, int W, bool SOLO, bool LONG>
 __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceWs ws) {
   constexpr int kE = 64 * VPL, NR = rows_ahead(VPL);
   __shared__ float part[W][kE];
@@ -221,8 +229,21 @@ __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceW
     for (int e = threadIdx.x; e < kE; e += 64 * W) hist[e] = 0;
     __syncthreads();
     float sum[VPL] = {};
+    int added = 0;
+    bool more = false;         // part holds sums of this wave's rows
+    auto fold = [&] {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        float& at = part[wave][expert_of<V>(lane, i)];
+        at = LONG && more ? at + sum[i] : sum[i];
+        sum[i] = 0.f;
+      }
+      more = true, added = 0;
+    };
     for (int r = mine; r < q.hi; r += W * NR) {
       if (r + NR <= q.lo) continue;
+      if (LONG && added == kFold) fold();
+      added += NR;
       if (r != held) {
         held = r;
 #pragma unroll
@@ -245,8 +266,7 @@ __global__ __launch_bounds__(64 * W) void balance_sums(BalanceParams p, BalanceW
       const int e = i == id_first ? first_id : p.ids[i];
       if (e >= 0 && e < p.E) atomicAdd(&hist[e], 1);
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) part[wave][expert_of<V>(lane, i)] = sum[i];
+    fold();
     __syncthreads();
     if constexpr (SOLO) {
       double share = 0.0;
@@ -415,8 +435,9 @@ template <int TYPE, int VPL, int V>
 hipError_t sums_for(const BalanceParams& p, const BalanceWs& ws, bool solo, hipStream_t s) {
   constexpr int W = VPL > 16 ? 4 : kSumWaves;   // LDS holds each wave's sums
   const unsigned n = ws.chunks > 0 ? ws.chunks : 1;
-  if (solo) balance_sums<TYPE, VPL, V, W, true><<<1, 64 * W, 0, s>>>(p, ws);
-  else balance_sums<TYPE, VPL, V, W, false><<<n, 64 * W, 0, s>>>(p, ws);
+  if (solo) balance_sums<TYPE, VPL, V, W, true, false><<<1, 64 * W, 0, s>>>(p, ws);
+  else if (ws.chunk <= W * kFold) balance_sums<TYPE, VPL, V, W, false, false><<<n, 64 * W, 0, s>>>(p, ws);
+  else balance_sums<TYPE, VPL, V, W, false, true><<<n, 64 * W, 0, s>>>(p, ws);
   return hipGetLastError();
 }
 
