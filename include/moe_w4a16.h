@@ -576,6 +576,8 @@ int64_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S);
  * with p the softmax of a row's logits, or their sigmoids over the sigmoids'
  * sum. A logit of -inf or NaN has p = 0, +inf counts as the largest FP32 value;
  * a row without other logits adds nothing to the sum of p.
+ * p of FP32 logits is right to a few 2^-24 of itself; of BF16 and FP16 logits
+ * its exponentials e^x are off by up to |x| 2^-24 besides.
  *   logits    device [T, E] of dtype, rows ld values apart (any alignment of
  *             the type); topk_ids device int32 [T, topk]
  *   loss      device float [S], counts device int32 [S, E], fully written
