@@ -18,6 +18,13 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kAhead = 4;    // rows of a lane whose loads are in flight together
 constexpr int kChunk = 256;  // rows: a round of loads
+constexpr int kStep = 8 * kWaves;   // rows that a workgroup's lanes take at a time
+// Values that FP32 adds up one after another; such sums are added in FP64 (4
+// million equal rows in one chain a lane were off by 2^-11). A group's rows go
+// through the whole workgroup's sum that many a lane at a time, because a second
+// set of sums in registers costs short groups more: 384 groups of 170 rows of
+// 2048 43 -> 45 us.
+constexpr int kFold = 256;
 
 struct Rows {
   int lo, hi;
@@ -33,7 +40,6 @@ __device__ __forceinline__ float column_sum(const BiasGradParams& p, int c0, int
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = c0 + 8 * (lane & 7);
   float sum[8] = {};
   if (col < p.N) {
-    constexpr int kStep = 8 * kWaves;   // rows of a round
     for (int64_t r = lo + wave * 8 + (lane >> 3); r < hi; r += kStep * kAhead) {
       Raw8<TYPE> raw[kAhead];
 #pragma unroll
@@ -79,7 +85,15 @@ __global__ __launch_bounds__(64 * kWaves) void bias_grad(BiasGradParams p, int o
   __shared__ float part[kWaves][64];
   const int wg = (int)(first + blockIdx.x), e = wg / blocks, c0 = (wg - e * blocks) * 64;
   const Rows g = group(p, e);
-  const float v = column_sum<TYPE>(p, c0, g.lo, g.hi, part);
+  float v = column_sum<TYPE>(p, c0, g.lo, min((int64_t)g.lo + kStep * kFold, (int64_t)g.hi), part);
+  if (g.hi - g.lo > kStep * kFold) {
+    double far = v;
+    for (int64_t r = (int64_t)g.lo + kStep * kFold; r < g.hi; r += kStep * kFold) {
+      __syncthreads();   // part is read
+      far += column_sum<TYPE>(p, c0, (int)r, min(r + kStep * kFold, (int64_t)g.hi), part);
+    }
+    v = (float)far;
+  }
   if (threadIdx.x < 64 && c0 + (int)threadIdx.x < p.N)
     store_any(p.db, (int64_t)e * p.db_ld + c0 + threadIdx.x, out_type, v);
 }
@@ -117,8 +131,21 @@ __global__ __launch_bounds__(64 * kWaves) void bias_grad_finish(BiasGradParams p
   float v = 0.f;
   if (g.lo < g.hi && col < p.N) {
     const float* from = static_cast<const float*>(p.ws) + (int64_t)e * p.N + col;
+    auto add_up = [&](int c, int last) {
 #pragma unroll 8
-    for (int c = g.lo / kChunk + wave; c <= (g.hi - 1) / kChunk; c += kWaves) v += from[(int64_t)c * p.N];
+      for (; c <= last; c += kWaves) v += from[(int64_t)c * p.N];
+    };
+    const int first = g.lo / kChunk, last = (g.hi - 1) / kChunk;
+    if (last - first < kWaves * kFold) {
+      add_up(first + wave, last);
+    } else {
+      double far = 0.0;
+      for (int c = first; c <= last; c += kWaves * kFold) {
+        add_up(c + wave, min(c + kWaves * kFold - 1, last));
+        far += v, v = 0.f;
+      }
+      v = (float)far;
+    }
   }
   part[wave][lane] = v;
   __syncthreads();
