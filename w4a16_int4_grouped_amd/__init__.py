@@ -807,6 +807,7 @@ def _offsets(t, device):
     if t is None:
         return None, 0
     _need(t.dim() == 1 and t.shape[0] >= 2, "offsets: [E + 1]")
+    _fits(t.shape[0])
     _dense(t, "offsets", _torch.int32, device, tuple(t.shape))
     return t.data_ptr(), t.shape[0] - 1
 
