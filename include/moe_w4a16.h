@@ -646,8 +646,9 @@ int32_t moe_mx8_scale_cols(int32_t K);
 
 /* Rows in 8 bits. A block's scale is 2^floor(log2 m) for its largest magnitude
  * m (at least 2^-127); codes are rounded to nearest even and end at -127 and
- * 127. They are exact in BF16, FP16 (within its range) and FP32. A block that
- * holds a NaN or an infinity becomes NaN (scale byte 255, codes 0).
+ * 127. They are exact in BF16, FP16 (within its range) and FP32, and off by up
+ * to max(m / 128, 2^-134). A block that holds a NaN or an infinity becomes NaN
+ * (scale byte 255, codes 0).
  *   x  device [rows, K] of dtype (BF16, FP16 or FP32), rows ld values apart;
  *      rows at most 2^40, rows * K at most 2^42
  * Errors: INVALID_ARG, HIP. */

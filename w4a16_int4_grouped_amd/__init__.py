@@ -971,7 +971,8 @@ def mx8_quant(x, out=None, stream=None):
     """Rows of x [rows, K] (bf16, fp16 or fp32, K a multiple of 8) in 8 bits:
     (codes int8 [rows, K], scales uint8 [rows, mx8_scale_cols(K)], one E8M0 byte
     per 32 values). A value is code * 2^(byte - 133), within a 128th of its
-    block's largest magnitude, and exact in bf16; a block with a NaN or an
+    block's largest magnitude or, for the smallest magnitudes, within 2^-134
+    (the least scale's half step), and exact in bf16; a block with a NaN or an
     infinity becomes NaN. `out` may give the two tensors."""
     torch = _torch or _load()
     _need(x.dim() == 2, "x: [rows, K]")
