@@ -528,6 +528,8 @@ enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 };
  *             values apart, or NULL
  *   residual  device [M, columns of out] of out_dtype, rows res_ld values
  *             apart, or NULL; may be `out` itself
+ * SwiGLU's sigmoid is off by up to (2 |gate| + 10) 2^-23 of itself, for FP32
+ * outputs too.
  * The residual's gradient is that of out; those of a, w and the bias are
  * moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad and moe_grouped_bias_grad for
  * the gradient before act (moe_swiglu_grad). Otherwise as moe_grouped_gemm. */
@@ -576,8 +578,9 @@ int64_t moe_router_balance_bytes(int32_t T, int32_t E, int32_t S);
  * with p the softmax of a row's logits, or their sigmoids over the sigmoids'
  * sum. A logit of -inf or NaN has p = 0, +inf counts as the largest FP32 value;
  * a row without other logits adds nothing to the sum of p.
- * p of FP32 logits is right to a few 2^-24 of itself; of BF16 and FP16 logits
- * its exponentials e^x are off by up to |x| 2^-24 besides.
+ * For FP32 logits the exponentials e^x and p are right to a few 2^-24 of
+ * themselves (softmax's x = l - max is rounded to FP32 once); for BF16 and FP16
+ * logits e^x is off by up to |x| 2^-24 besides.
  *   logits    device [T, E] of dtype, rows ld values apart (any alignment of
  *             the type); topk_ids device int32 [T, topk]
  *   loss      device float [S], counts device int32 [S, E], fully written
@@ -676,8 +679,9 @@ moe_status_t moe_mx8_dequant(const int8_t* q, const uint8_t* scales, int64_t row
  *   scales  device uint8 [rows, 2, moe_mx8_scale_cols(inter)]
  *   offsets device int32 [E + 1] or NULL: only rows [offsets[0], offsets[E])
  *           are read and written
- * inter is a multiple of 8 up to 2^19, rows up to 2^30, E 1..4096. Errors:
- * INVALID_ARG, HIP. */
+ * The sigmoid (0 where e^-g ends FP32) is right to a few 2^-24 of itself for FP32
+ * rows, for others off by up to (2 |g| + 10) 2^-23. inter is a multiple of 8 up to 2^19, rows up to 2^30,
+ * E 1..4096. Errors: INVALID_ARG, HIP. */
 moe_status_t moe_swiglu_save(const void* h, int32_t dtype, int64_t h_ld, int32_t rows,
                              int32_t inter, const int32_t* offsets, int32_t E, void* a,
                              int64_t a_ld, int8_t* q, uint8_t* scales, moe_stream_t stream);

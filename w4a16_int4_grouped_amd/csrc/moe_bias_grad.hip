@@ -3,7 +3,8 @@
 // A workgroup sums 64 columns of one group: 8 lanes lie along a row (16 bytes
 // each, a line), the others and the waves along the rows, whose sums meet in a
 // fixed order. HBM bounds it where there are enough groups and columns: 24576
-// rows of 4096 in 48 groups 34 us (6.0 TB/s). A workgroup alone reads some 60 to 90 GB/s:
+// rows of 4096 in 48 even groups 34 to 37 us (5.4 to 5.9 TB/s), uneven ones on
+// other rows at each call 39. A workgroup alone reads some 60 to 90 GB/s:
 // where groups are few and long, the rows are cut into chunks, a workgroup sums
 // 64 columns of a chunk for each group in it, and a second kernel adds the
 // chunks' sums up. Part c + e of the workspace belongs to chunk c and group e; no
@@ -164,8 +165,9 @@ int64_t chunks_of(int M) { return ((int64_t)M + kChunk - 1) / kChunk; }
 //   1, 4096, 512     7.8 / 4.9*      1, 24576, 512    73 / 7.8*       8, 24576, 64     9.2 / 5.6*
 //   2, 4096, 7168    12* / 13        1, 24576, 4096   93 / 36*        8, 16384, 4096   25* / 25
 //   16, 8192, 1024   4.2* / 6.7      48, 24576, 4096  37* / 37        8, 448, 4096     3.4* / 9.7
-// The rule takes the rows as even over the groups: where one of many has most of
-// them, it alone takes as long as a single group.
+// (4 groups of 2048 rows of 1024 take the slower side.) The rule takes the rows as
+// even over the groups: where one of many has most of them, it alone takes as long
+// as a single group: nine tenths of 24576 rows of 4096 with one of 48 86 us.
 bool cut(int E, int M, int N) {
   const double bytes = (double)M * N * 2 / 5.5e6, waves = (double)E * ((N + 63) / 64) / 512;
   const double alone = (double)M / E * 128 / 60e3 * (waves > 1 ? waves : 1);

@@ -14,8 +14,8 @@
 // without values. All four kernels pass once over their data and are bound by it
 // (a large copy runs at 4.95 TB/s here, a fill at 6.8), BF16:
 //   mx8_quant    8192 rows of 7168: 31 us, 5.7 TB/s
-//   mx8_dequant  as 68288 rows of a routing: 212 to 222 us, 6.4 TB/s, a third of
-//                it codes that a token's eight rows read in eight XCDs
+//   mx8_dequant  as 68288 rows of a routing: 212 to 222 us, 6.6 to 6.9 TB/s, a
+//                third of it codes that a token's eight rows read in eight XCDs
 //   swiglu_save  65536 rows of 2 x 2048: 180 us, 6.0 TB/s
 //   swiglu_grad  the same, from 8 bits: 232 us, 5.9 TB/s
 // A thread's loads all stand before its first conversion, so that they are in
