@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include "moe_device.h"
+#include "moe_grid.h"
 #include "moe_launch.h"
 
 namespace moe {
@@ -20,8 +21,8 @@ namespace {
 __global__ __launch_bounds__(256) void repack_words(const uint32_t* __restrict__ canon,
                                                     u32x4_t* __restrict__ prep, int N, int K,
                                                     int RG, int Kc, int interleave_I,
-                                                    size_t total) {
-  const size_t idx = (size_t)blockIdx.x * 256 + threadIdx.x;
+                                                    size_t total, uint32_t first) {
+  const size_t idx = ((size_t)first + blockIdx.x) * 256 + threadIdx.x;
   if (idx >= total) return;
   const int lane = (int)(idx & 63);
   size_t t = idx >> 6;
@@ -42,8 +43,9 @@ __global__ __launch_bounds__(256) void repack_words(const uint32_t* __restrict__
 __global__ __launch_bounds__(256) void repack_scales(const uint16_t* __restrict__ canon,
                                                      uint16_t* __restrict__ prep, int N, int K,
                                                      int RG, int Kc, int interleave_I,
-                                                     size_t total, int32_t* __restrict__ bad) {
-  const size_t idx = (size_t)blockIdx.x * 256 + threadIdx.x;
+                                                     size_t total, int32_t* __restrict__ bad,
+                                                     uint32_t first) {
+  const size_t idx = ((size_t)first + blockIdx.x) * 256 + threadIdx.x;
   if (idx >= total) return;
   const int mt = (int)(idx & 3);
   const int lane = (int)((idx >> 2) & 63);
@@ -118,16 +120,19 @@ hipError_t zero_words(uint32_t* p, size_t n, hipStream_t s) {
 
 hipError_t launch_repack(const MatLayout& m, const int32_t* words, const uint16_t* scales,
                          char* prepared, int32_t* bad_scale_flag, hipStream_t s) {
-  const size_t nw = (size_t)m.E * m.RG * m.Kc * kMT * 64;
-  hipLaunchKernelGGL(repack_words, dim3((unsigned)((nw + 255) / 256)), dim3(256), 0, s,
-                     reinterpret_cast<const uint32_t*>(words),
-                     reinterpret_cast<u32x4_t*>(prepared + m.off_words), m.N, m.K, m.RG, m.Kc,
-                     m.interleave_I, nw);
-  const size_t ns = (size_t)m.E * m.RG * m.Kc * 64 * kMT;
-  hipLaunchKernelGGL(repack_scales, dim3((unsigned)((ns + 255) / 256)), dim3(256), 0, s, scales,
-                     reinterpret_cast<uint16_t*>(prepared + m.off_scales), m.N, m.K, m.RG, m.Kc,
-                     m.interleave_I, ns, bad_scale_flag);
-  return hipGetLastError();
+  const size_t n = (size_t)m.E * m.RG * m.Kc * kMT * 64;   // 16-byte pieces of words, and scales
+  const int64_t blocks = (int64_t)((n + 255) / 256);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  return in_slices(blocks, 256, [&](uint32_t first, uint32_t g) {
+    hipLaunchKernelGGL(repack_words, dim3(g), dim3(256), 0, s,
+                       reinterpret_cast<const uint32_t*>(words),
+                       reinterpret_cast<u32x4_t*>(prepared + m.off_words), m.N, m.K, m.RG, m.Kc,
+                       m.interleave_I, n, first);
+    hipLaunchKernelGGL(repack_scales, dim3(g), dim3(256), 0, s, scales,
+                       reinterpret_cast<uint16_t*>(prepared + m.off_scales), m.N, m.K, m.RG, m.Kc,
+                       m.interleave_I, n, bad_scale_flag, first);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_dequant_expert(const MatLayout& m, const char* prepared, int expert,
